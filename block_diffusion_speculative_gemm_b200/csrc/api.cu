@@ -236,13 +236,6 @@ bool config_supported(const dflash_config& c) {
 int qkv_out(const dflash_config& c) { return (c.n_q + 2 * c.n_kv) * c.head_dim; }
 
 // ---------------------------------------------------------------- workspace layout
-// Workspace header: the device error word (byte 0), then 32768 completion
-// counters: verify uses one per request, the draft attention one per
-// (request, kv head).  No call writes the header except through those words,
-// every call leaves the counters it used at zero (calls sharing a workspace
-// never overlap), and each call's own buffers start after the header.
-constexpr size_t kCntOff = 256;
-constexpr size_t kHeader = kCntOff + (size_t(128) << 10);
 constexpr int kMaxChunks = 64;
 int g_attn_chunk = 0;  // split-KV chunk override in keys (tests and tuning; 0 = rule)
 // GEMM schedules.  0 (default): the LM head streams K evenly over all workers

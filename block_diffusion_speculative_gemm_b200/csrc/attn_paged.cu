@@ -1,0 +1,566 @@
+// Paged chunk attention for few rows per kv head (single tokens, drafted
+// blocks): softmax(scale Q K^T) V over a paged cache in one pass, on
+// mma.sync m16n8k16 with fp32 accumulators.
+//
+//   S = Q K^T;  m' = max(m, max S);  P = 2^(S c - m' c), c = scale log2(e);
+//   l' = l 2^((m - m') c) + sum P;   O' = O 2^((m - m') c) + P V
+//
+// A CTA is one producer warp, which streams 64-key K and V tiles into a ring
+// of shared-memory slots with TMA (one box per page piece), and four compute
+// warps.  16 WM rows of an item go to WM warps; the 4 / WM warps that share
+// rows split the keys of every tile and are joined at the end of a segment.
+// The softmax state and O stay in registers, Q too, P goes from the S
+// accumulators to the next product's operand without leaving the thread.
+// Bound by memory: the keys and values of an item are read once for all its
+// rows, 4 rows flop per byte.  The producer runs on over segment boundaries,
+// so the ring stays full while a segment is finished.
+//
+// Every CTA has the same number of key tiles (attn_paged.cuh); an item shared
+// by several CTAs is left as partials (O, max, sum), and the CTA that counts
+// itself last joins them in CTA order, so results do not depend on timing.
+#include <algorithm>
+
+#include "attn_paged.cuh"
+
+namespace dflash {
+
+namespace {
+
+constexpr int kKT = 64;                   // keys per tile
+constexpr int kCompute = 128;             // compute threads
+constexpr int kThreads = kCompute + 32;
+constexpr int kSlots = 6;                 // ring slots, each a K or a V tile
+constexpr int kPassCols = 64;             // O columns joined at a time
+
+template <int HD> constexpr int slot_bytes() { return kKT * HD * 2; }
+template <int WM> constexpr int scratch_bytes() { return (4 / WM - 1) * WM * 16 * kPassCols * 4; }
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4],
+                                                 uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4],
+                                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void bar_compute() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
+}
+// The same barrier; true on every thread when any thread brought `v` true.
+__device__ __forceinline__ bool bar_compute_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kCompute)
+      : "memory");
+  return r != 0;
+}
+
+template <typename T, int HD, int WM>
+__global__ void __launch_bounds__(kThreads, 2)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ PagedAttnArgs a, int box) {
+  pdl_trigger();
+  constexpr int NK = 4 / WM;          // key groups
+  constexpr int KW = kKT / NK;        // keys of a tile per warp
+  constexpr int kNT = KW / 8;         // S column blocks
+  constexpr int kSlot = slot_bytes<HD>();
+  constexpr int kHalfTile = kKT * 128;  // one 64-column half of a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  float* scratch = reinterpret_cast<float*>(smem + kSlots * kSlot);
+  long long* pre = reinterpret_cast<long long*>(smem + kSlots * kSlot + scratch_bytes<WM>());
+  __shared__ __align__(8) uint64_t bars[2 * kSlots];
+  __shared__ float s_ml[4][16][2];
+  __shared__ int s_abort, s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t s_base = smem_u32(smem);
+  auto full = [&](int s) { return smem_u32(&bars[s]); };
+  auto empty = [&](int s) { return smem_u32(&bars[kSlots + s]); };
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 4);
+    }
+    fence_barrier_init();
+    s_abort = 0;
+  }
+  pdl_wait();
+  attn_plan<HD, kKT>(a, pre);  // ends with a barrier
+
+  // a bounded wait that also gives up once another warp has given up
+  auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(b, parity)) {
+      if (*(volatile int*)&s_abort || global_ns() - t0 > kWaitNs) {
+        *(volatile int*)&s_abort = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+  bool ok = true;
+  AttnWalk<kKT> w(a, pre);
+  const int rows_all = a.n_pages * a.nkv * a.page;  // a row past the pools: TMA fills zeros
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    const uint64_t pol = policy_evict_first();
+    const int per = kKT / box;  // boxes per tile
+    int it = 0;                 // ring position
+    for (; !w.done() && ok; w.next()) {
+      const int32_t* tab = a.table + (int64_t)w.r * a.max_pages;
+      int ent = 0, ent_base = -1;
+      for (int kt = w.kbeg; kt < w.kend && ok; ++kt) {
+        // the pool rows of the tile's boxes, looked up 32 boxes at a time
+        const int b0 = (kt - w.kbeg) * per;
+        if (ent_base < 0 || b0 + per > ent_base + 32) {
+          ent_base = b0;
+          const int key = w.kbeg * kKT + (b0 + lane) * box;
+          int y = rows_all;
+          if (key < w.q.len) {
+            const int e = tab[key / a.page];
+            if (e >= 0 && e < a.n_pages) y = (e * a.nkv + w.h) * a.page + key % a.page;
+          }
+          if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
+          ent = y;
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int s = it % kSlots;
+          if (it >= kSlots) {
+            ok = __all_sync(0xffffffffu, wait(empty(s), ((it / kSlots) - 1) & 1));
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full(s), kSlot);
+          __syncwarp();
+          for (int b = 0; b < per; ++b) {
+            const int y = __shfl_sync(0xffffffffu, ent, b0 + b - ent_base);
+            if (lane == 0) {
+              const uint32_t dst = s_base + s * kSlot + b * box * 128;
+#pragma unroll
+              for (int hf = 0; hf < HD / 64; ++hf)
+                tma_load_2d(dst + hf * kHalfTile, kv ? &tmV : &tmK, full(s), hf * 64, y, pol);
+            }
+          }
+        }
+      }
+    }
+    // the copies in flight land before the CTA may end
+    for (int j = max(0, it - kSlots); j < it; ++j) ok &= mbar_wait(full(j % kSlots), (j / kSlots) & 1);
+  } else {
+    // ------------------------------------------------------------ compute
+    const int wm = warp % WM, wk = warp / WM;
+    const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+    const T* qg = static_cast<const T*>(a.q);
+    // ldmatrix addresses: K rows are keys (operand as stored), V transposed
+    const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+    const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+    int it = 0, checked = -1;
+    bool mapped = false;
+    for (; !w.done() && ok; w.next()) {
+      if (w.r != checked) {
+        checked = w.r;
+        mapped = pages_mapped(a, w.r, w.q, lane);
+        if (!mapped && lane == 0) set_error(a.err, DFLASH_DEV_PAGE);
+      }
+      const int tok0 = w.t * a.ipt, R = w.tokens() * a.G;
+      // this thread's two rows: token, query head within the group
+      int row[2], tok[2], hg[2], lo[2], hi[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        row[j] = wm * 16 + g8 + 8 * j;
+        const int rr = min(row[j], R - 1);
+        tok[j] = tok0 + rr / a.G;
+        hg[j] = rr % a.G;
+        lo[j] = row_lo(a, w.q.st + tok[j]);
+        hi[j] = row_hi(a, w.q, w.q.st + tok[j]);
+      }
+      uint32_t qf[HD / 16][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const T* src = qg + (int64_t)(w.q.row0 + tok[j]) * a.q_stride +
+                       (int64_t)(w.h * a.G + hg[j]) * HD + t2;
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          qf[ks][j] = *reinterpret_cast<const uint32_t*>(src + ks * 16);
+          qf[ks][j + 2] = *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8);
+        }
+      }
+      // every row of the item sees the keys [all_lo, all_hi)
+      const int all_hi = row_hi(a, w.q, w.q.st + tok0);
+      const int all_lo = row_lo(a, w.q.st + tok0 + w.tokens() - 1);
+      float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+      for (int kt = w.kbeg; kt < w.kend && ok; ++kt, it += 2) {
+        const int sk = it % kSlots, sv = (it + 1) % kSlots;
+        if (!__all_sync(0xffffffffu, wait(full(sk), (it / kSlots) & 1))) { ok = false; break; }
+        const int key0 = kt * kKT + wk * KW;  // this warp's first key
+        const uint32_t kb = s_base + sk * kSlot + (uint32_t)(wk * KW) * 128;
+        float sc[kNT][4];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks)
+#pragma unroll
+          for (int n = 0; n < kNT; n += 2) {
+            uint32_t b[4];
+            const int rr = n * 8 + kr, ch = (ks & 3) * 2 + kc;
+            ldsm4(b, kb + (ks >> 2) * kHalfTile + rr * 128 + ((ch ^ (rr & 7)) << 4));
+            mma16816<T>(sc[n], qf[ks], b[0], b[1]);
+            mma16816<T>(sc[n + 1], qf[ks], b[2], b[3]);
+          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(sk));
+        if (key0 < all_lo || key0 + KW > all_hi) {
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + n * 8 + t2 + (e & 1);
+              if (key < lo[e >> 1] || key >= hi[e >> 1]) sc[n][e] = -INFINITY;
+            }
+        }
+        float alpha[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = m[j];
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+            mx = fmaxf(mx, fmaxf(sc[n][2 * j], sc[n][2 * j + 1]) * a.scale_log2);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          alpha[j] = ex2_ftz(m[j] - ref);  // 0 while nothing was seen
+          m[j] = mx;
+          l[j] *= alpha[j];
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float pv = ex2_ftz(fmaf(sc[n][2 * j + e], a.scale_log2, -ref));
+              sc[n][2 * j + e] = pv;
+              l[j] += pv;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e >> 1];
+
+        if (!__all_sync(0xffffffffu, wait(full(sv), ((it + 1) / kSlots) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint32_t vb = s_base + sv * kSlot + (uint32_t)(wk * KW) * 128;
+        const bool tail = key0 + KW > w.q.len;
+#pragma unroll
+        for (int k2 = 0; k2 < KW / 16; ++k2) {
+          // P rounded to the operand type: relative error at most half a step per weight
+          const uint32_t pf[4] = {
+              pack2<T>(sc[2 * k2][0], sc[2 * k2][1]), pack2<T>(sc[2 * k2][2], sc[2 * k2][3]),
+              pack2<T>(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]),
+              pack2<T>(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3])};
+          // rows past the request's keys hold whatever the page held: as zeros
+          // they add nothing (their weights are 0, but 0 x NaN is not)
+          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+          if (tail)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = key0 + k2 * 16 + j * 8 + t2;
+              keep[j] = key + 1 < w.q.len ? 0xffffffffu : key < w.q.len ? 0xffffu : 0u;
+            }
+#pragma unroll
+          for (int d = 0; d < HD / 16; ++d) {
+            uint32_t b[4];
+            const int rr = k2 * 16 + vr, ch = (d & 3) * 2 + vc;
+            ldsm4t(b, vb + (d >> 2) * kHalfTile + rr * 128 + ((ch ^ (rr & 7)) << 4));
+            if (tail) {
+              b[0] &= keep[0];
+              b[1] &= keep[1];
+              b[2] &= keep[0];
+              b[3] &= keep[1];
+            }
+            mma16816<T>(o[2 * d], pf, b[0], b[1]);
+            mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(sv));
+      }
+      // ---------------------------------------------------------- end of a segment
+      // a wait that gave up ends all compute warps here, together
+      if (bar_compute_or(!ok)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+        l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+      }
+      if (NK > 1) {  // join the key groups
+        if ((lane & 3) == 0)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            s_ml[warp][g8 + 8 * j][0] = m[j];
+            s_ml[warp][g8 + 8 * j][1] = l[j];
+          }
+        bar_compute();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int k = 0; k < NK; ++k) M = fmaxf(M, s_ml[k * WM + wm][g8 + 8 * j][0]);
+          const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+            L += s_ml[k * WM + wm][g8 + 8 * j][1] * ex2_ftz(s_ml[k * WM + wm][g8 + 8 * j][0] - ref);
+          const float f = ex2_ftz(m[j] - ref);
+          m[j] = M;
+          l[j] = L;
+#pragma unroll
+          for (int i = 0; i < HD / 8; ++i) {
+            o[i][2 * j] *= f;
+            o[i][2 * j + 1] *= f;
+          }
+        }
+#pragma unroll
+        for (int pass = 0; pass < HD / kPassCols; ++pass) {
+          constexpr int kB = kPassCols / 8;
+          if (wk > 0) {
+            float* dst = scratch + (size_t)((wk - 1) * WM + wm) * 16 * kPassCols;
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<float2*>(dst + (g8 + 8 * j) * kPassCols + i * 8 + t2) =
+                    make_float2(o[pass * kB + i][2 * j], o[pass * kB + i][2 * j + 1]);
+          }
+          bar_compute();
+          if (wk == 0) {
+#pragma unroll
+            for (int k = 1; k < NK; ++k) {
+              const float* src = scratch + (size_t)((k - 1) * WM + wm) * 16 * kPassCols;
+#pragma unroll
+              for (int i = 0; i < kB; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float2 v = *reinterpret_cast<const float2*>(
+                      src + (g8 + 8 * j) * kPassCols + i * 8 + t2);
+                  o[pass * kB + i][2 * j] += v.x;
+                  o[pass * kB + i][2 * j + 1] += v.y;
+                }
+            }
+          }
+          bar_compute();
+        }
+      }
+      const bool whole = w.whole();
+      T* outp = static_cast<T*>(a.out);
+      if (wk == 0) {
+        unsigned odd[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          bool fin = true;
+#pragma unroll
+          for (int i = 0; i < HD / 8; ++i) fin &= isfinite(o[i][2 * j]) && isfinite(o[i][2 * j + 1]);
+          odd[j] = __ballot_sync(0xffffffffu, !fin && row[j] < R && !isnan(l[j]));
+          if (row[j] >= R) continue;
+          if (whole) {
+            if (mapped) {
+              const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+              T* dst = outp + (int64_t)(w.q.row0 + tok[j]) * a.out_stride +
+                       (int64_t)(w.h * a.G + hg[j]) * HD + t2;
+#pragma unroll
+              for (int i = 0; i < HD / 8; ++i)
+                *reinterpret_cast<uint32_t*>(dst + i * 8) =
+                    pack2<T>(o[i][2 * j] * inv, o[i][2 * j + 1] * inv);
+              if (a.lse && (lane & 3) == 0)
+                a.lse[(int64_t)(w.q.row0 + tok[j]) * a.nq + w.h * a.G + hg[j]] =
+                    l[j] == 0.f ? -INFINITY : (m[j] + log2f(l[j])) * 0.6931471805599453f;
+            }
+          } else {
+            const size_t pr = (size_t)w.slot() * a.tile_rows + row[j];
+#pragma unroll
+            for (int i = 0; i < HD / 8; ++i)
+              *reinterpret_cast<float2*>(a.part_o + pr * HD + i * 8 + t2) =
+                  make_float2(o[i][2 * j], o[i][2 * j + 1]);
+            if ((lane & 3) == 0)
+              *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m[j], l[j]);
+          }
+        }
+        __syncwarp();
+        if ((odd[0] | odd[1]) && mapped) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            // four lanes hold a row: take each row once
+            for (int rr = 0; rr < 8; ++rr) {
+              if (((odd[j] >> (rr * 4)) & 15) == 0) continue;
+              const float mr = __shfl_sync(0xffffffffu, m[j], rr * 4);
+              const float lr = __shfl_sync(0xffffffffu, l[j], rr * 4);
+              const int tk = __shfl_sync(0xffffffffu, tok[j], rr * 4);
+              const int hh = __shfl_sync(0xffffffffu, hg[j], rr * 4);
+              const int pr = __shfl_sync(0xffffffffu, row[j], rr * 4);
+              float acc[HD / 32];
+              if (!masked_key_fallback<T, HD, kKT>(a, w.r, w.h, w.q, w.kbeg, w.kend, tk, hh,
+                                                   mr == -INFINITY ? 0.f : mr, lane, acc))
+                continue;
+#pragma unroll
+              for (int d = 0; d < HD / 32; ++d) {
+                const int col = lane * (HD / 32) + d;
+                if (whole)
+                  outp[(int64_t)(w.q.row0 + tk) * a.out_stride +
+                       (int64_t)(w.h * a.G + hh) * HD + col] =
+                      from_f<T>(lr == 0.f ? 0.f : acc[d] / lr);
+                else
+                  a.part_o[((size_t)w.slot() * a.tile_rows + pr) * HD + col] = acc[d];
+              }
+            }
+        }
+      }
+      if (!whole) {
+        // the CTA that finishes last joins the item's partials in CTA order
+        __threadfence();
+        bar_compute();
+        const int c0 = w.cta_first(), c1 = w.cta_last(), late = w.later_in(c0);
+        auto slot_row = [&](int x, int rr) {
+          return (size_t)(2 * x + (x == c0 ? late : 0)) * a.tile_rows + rr;
+        };
+        if (tid == 0) {
+          const unsigned old = atomicAdd(a.cnt + c0, 1u);
+          s_last = old == (unsigned)(c1 - c0);
+          if (s_last) a.cnt[c0] = 0;
+        }
+        bar_compute();
+        if (s_last && mapped) {
+          __threadfence();
+          for (int idx = tid; idx < R * (HD / 4); idx += kCompute) {
+            const int rr = idx / (HD / 4), c4 = (idx % (HD / 4)) * 4;
+            float M = -INFINITY;
+            for (int x = c0; x <= c1; ++x)
+              M = fmaxf(M, __ldcg(a.part_ml + slot_row(x, rr) * 2));
+            const float ref = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int x = c0; x <= c1; ++x) {
+              const size_t pr = slot_row(x, rr);
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + pr * 2));
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * HD + c4));
+              const float f = ex2_ftz(ml.x - ref);
+              L += ml.y * f;
+              s.x += v.x * f;
+              s.y += v.y * f;
+              s.z += v.z * f;
+              s.w += v.w * f;
+            }
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const int tk = tok0 + rr / a.G, hh = w.h * a.G + rr % a.G;
+            uint2 u;
+            u.x = pack2<T>(s.x * inv, s.y * inv);
+            u.y = pack2<T>(s.z * inv, s.w * inv);
+            *reinterpret_cast<uint2*>(outp + (int64_t)(w.q.row0 + tk) * a.out_stride +
+                                      (int64_t)hh * HD + c4) = u;
+            if (a.lse && c4 == 0)
+              a.lse[(int64_t)(w.q.row0 + tk) * a.nq + hh] =
+                  L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;
+          }
+        }
+        bar_compute();  // s_last is reused
+      }
+    }
+  }
+  if (!ok && lane == 0) set_error(a.err, DFLASH_DEV_TIMEOUT);
+}
+
+template <typename T, int HD, int WM>
+int launch_one(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int box,
+               cudaStream_t s) {
+  const size_t smem = 1024 + (size_t)kSlots * slot_bytes<HD>() + scratch_bytes<WM>() +
+                      (size_t)a.batch * 8;
+  static SmemLimit limit;
+  if (!limit.raise(reinterpret_cast<const void*>(attn_paged_kernel<T, HD, WM>),
+                   1024 + kSlots * slot_bytes<HD>() + scratch_bytes<WM>() + kAttnMaxBatch * 8))
+    return DFLASH_ECUDA;
+  const cudaError_t e = launch_pdl(attn_paged_kernel<T, HD, WM>, dim3(attn_paged_ctas()),
+                                   dim3(kThreads), smem, s, 1, tk, tv, a, box);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ECUDA;
+}
+
+template <typename T, int HD>
+int launch_rows(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int box,
+                cudaStream_t s) {
+  if (a.tile_rows == 16) return launch_one<T, HD, 1>(a, tk, tv, box, s);
+  if (a.tile_rows == 32) return launch_one<T, HD, 2>(a, tk, tv, box, s);
+  return launch_one<T, HD, 4>(a, tk, tv, box, s);
+}
+
+}  // namespace
+
+int attn_paged_ctas() { return 2 * num_sms(); }
+
+int launch_attn_paged(const PagedAttnArgs& a, int hd, int dtype, cudaStream_t s) {
+  // boxes of whole pages, or of the tile where a page holds it
+  const int box = std::min(a.page, kKT);
+  const int64_t rows = (int64_t)a.n_pages * a.nkv * a.page;
+  CUtensorMap tk, tv;
+  if (!encode_2d(&tk, a.k_pool, rows, hd, hd, box, dtype) ||
+      !encode_2d(&tv, a.v_pool, rows, hd, hd, box, dtype))
+    return DFLASH_ECUDA;
+  TimedScope ts(s, TC_ATTN);
+  if (dtype == DFLASH_BF16)
+    return hd == 128 ? launch_rows<__nv_bfloat16, 128>(a, tk, tv, box, s)
+                     : launch_rows<__nv_bfloat16, 64>(a, tk, tv, box, s);
+  return hd == 128 ? launch_rows<__half, 128>(a, tk, tv, box, s)
+                   : launch_rows<__half, 64>(a, tk, tv, box, s);
+}
+
+}  // namespace dflash

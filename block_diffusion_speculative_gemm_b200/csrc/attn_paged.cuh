@@ -1,0 +1,352 @@
+// Paged chunk attention, shared by its kernels: the call's arguments, which
+// keys a row sees, and the division of the work.
+//
+// A request's rows are its new tokens x the G = n_q / n_kv query heads of a kv
+// head, packed token-major (row i * G + g), so that one pass over a kv head's
+// keys serves all of them.  An item is (request, kv head, tile of `ipt` tokens)
+// and costs as many units as it has key tiles.  The units of all items, in
+// order, are cut into one equal range per CTA: every CTA streams the same
+// number of key tiles however ragged the batch is, at most two of its items
+// are shared with other CTAs (its first and its last), and nothing about the
+// lengths has to be known on the host.  A CTA finds its range by summing the
+// batch's units itself, which costs one pass over the lengths and saves a
+// planning launch.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dflash {
+
+struct PagedAttnArgs {
+  const void* q;
+  int64_t q_stride;
+  const int32_t *cu, *start, *kv_len;  // kv_len null: start + rows
+  int batch, n_rows, nq, nkv, G;
+  const int32_t* table;
+  int max_pages, page, n_pages;
+  float scale_log2;  // score scale times log2(e)
+  int causal, window;
+  void* out;
+  int64_t out_stride;
+  float* lse;        // [n_rows][nq] or null
+  int ipt;           // tokens per item
+  int tile_rows;     // rows of an item's partial (>= ipt * G)
+  float *part_o, *part_ml;  // slot s: [tile_rows][HD] and [tile_rows][2] (max in log2 units, sum)
+  unsigned* cnt;     // one zeroed counter per CTA
+  int32_t* err;
+  const void *k_pool, *v_pool;
+};
+
+struct AttnReq {
+  int row0, n, st, len;
+};
+
+// Request r's lengths; the return value is DFLASH_OK's 0 or the error bits of
+// a request that must not be touched.
+__device__ __forceinline__ int attn_req(const PagedAttnArgs& a, int r, AttnReq& q) {
+  q.row0 = a.cu[r];
+  const int end = a.cu[r + 1];
+  q.st = a.start[r];
+  if (q.row0 < 0 || end < q.row0 || end > a.n_rows) return DFLASH_DEV_ROWS;
+  q.n = end - q.row0;
+  const int64_t last = (int64_t)q.st + q.n;
+  const int64_t len = a.kv_len ? (int64_t)a.kv_len[r] : last;
+  if (q.st < 0 || last > 0x7fffffff || len < 0 || len > (int64_t)a.max_pages * a.page)
+    return DFLASH_DEV_CTX_CAP;
+  q.len = (int)len;
+  return 0;
+}
+
+// Keys [lo, hi) that a token at position p sees.
+__device__ __forceinline__ int row_lo(const PagedAttnArgs& a, int p) {
+  return a.window > 0 ? max(0, p - a.window + 1) : 0;
+}
+__device__ __forceinline__ int row_hi(const PagedAttnArgs& a, const AttnReq& q, int p) {
+  return a.causal ? min(q.len, p + 1) : q.len;
+}
+
+// Key tiles [k0, k1) of item tile t (empty when no row of it sees a key).
+template <int KT>
+__device__ __forceinline__ void tile_range(const PagedAttnArgs& a, const AttnReq& q, int t, int& k0,
+                                           int& k1) {
+  const int i0 = t * a.ipt, i1 = min(q.n, i0 + a.ipt);
+  const int lo = row_lo(a, q.st + i0), hi = row_hi(a, q, q.st + i1 - 1);
+  k0 = lo / KT;
+  k1 = hi > lo ? (hi - 1) / KT + 1 : k0;
+}
+
+__device__ __forceinline__ int attn_tiles(const PagedAttnArgs& a, int n) {
+  return (n + a.ipt - 1) / a.ipt;
+}
+
+// Rows of item tile t that see no key: output 0, log-sum-exp -inf.  Called by a warp.
+template <int HD>
+__device__ void zero_rows(const PagedAttnArgs& a, const AttnReq& q, int t, int lane) {
+  const int i0 = t * a.ipt, i1 = min(q.n, i0 + a.ipt);
+  for (int i = i0; i < i1; ++i) {
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                        (int64_t)(q.row0 + i) * a.out_stride);
+    for (int c = lane; c < a.nq * HD / 8; c += 32) o[c] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int c = lane; c < a.nq; c += 32) a.lse[(int64_t)(q.row0 + i) * a.nq + c] = -INFINITY;
+  }
+}
+
+// True when every page that request q's rows may read is mapped.  Called by a
+// warp; the answer is the same in every CTA that works on the request.
+__device__ __forceinline__ bool pages_mapped(const PagedAttnArgs& a, int r, const AttnReq& q,
+                                             int lane) {
+  const int lo = row_lo(a, q.st), hi = row_hi(a, q, q.st + q.n - 1);
+  bool bad = false;
+  if (hi > lo) {
+    const int32_t* tab = a.table + (int64_t)r * a.max_pages;
+    const int last = (hi - 1) / a.page;
+#pragma unroll 4
+    for (int k = lo / a.page + lane; k <= last; k += 32) {
+      const int e = tab[k];
+      bad |= e < 0 || e >= a.n_pages;
+    }
+  }
+  return !__any_sync(0xffffffffu, bad);
+}
+
+// Largest batch of a call: the prefix sums of every request sit in shared memory.
+constexpr int kAttnMaxBatch = 4096;
+
+// Fills pre[r] with the units of requests 0..r (every thread of the CTA; ends
+// with a barrier).  Requests with bad lengths have none and set their error
+// bits; items without keys have none and are written here, by one CTA each.
+template <int HD, int KT>
+__device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nthr = blockDim.x, nw = nthr >> 5;
+  constexpr int kFew = 4;  // item tiles a single thread adds up
+  bool spread = false;
+  for (int r = tid; r < a.batch; r += nthr) {
+    AttnReq q;
+    long long u = 0;
+    const int bad = attn_req(a, r, q);
+    if (bad) {
+      if ((int)(r % gridDim.x) == (int)blockIdx.x) set_error(a.err, bad);
+    } else {
+      const int nt = attn_tiles(a, q.n);
+      bool empty = false;
+      for (int t = 0; t < min(nt, kFew); ++t) {
+        int k0, k1;
+        tile_range<KT>(a, q, t, k0, k1);
+        u += k1 - k0;
+        empty |= k1 == k0;
+      }
+      if (nt > kFew || empty) {
+        u = -1;
+        spread = true;
+      }
+    }
+    pre[r] = u;
+  }
+  if (__syncthreads_or(spread)) {
+    for (int r = warp; r < a.batch; r += nw) {
+      if (pre[r] >= 0) continue;
+      AttnReq q;
+      attn_req(a, r, q);
+      const int nt = attn_tiles(a, q.n);
+      const bool mine = (int)(r % gridDim.x) == (int)blockIdx.x;
+      long long u = 0;
+      for (int t0 = 0; t0 < nt; t0 += 32) {
+        int k0 = 0, k1 = 0;
+        if (t0 + lane < nt) tile_range<KT>(a, q, t0 + lane, k0, k1);
+        u += k1 - k0;
+        if (mine) {
+          unsigned e = __ballot_sync(0xffffffffu, t0 + lane < nt && k1 == k0);
+          if (e && !pages_mapped(a, r, q, lane)) e = 0;
+          for (; e; e &= e - 1) zero_rows<HD>(a, q, t0 + __ffs(e) - 1, lane);
+        }
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+      __syncwarp();
+      if (lane == 0) pre[r] = u;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    long long carry = 0;
+    for (int r0 = 0; r0 < a.batch; r0 += 32) {
+      const int r = r0 + lane;
+      long long v = r < a.batch ? pre[r] * a.nkv : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += w;
+      }
+      v += carry;
+      if (r < a.batch) pre[r] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// The CTA whose range holds unit u, when W units are cut into N ranges
+// [W c / N, W (c + 1) / N).
+__device__ __forceinline__ int cta_of_unit(long long u, long long W, int N) {
+  return (int)(((u + 1) * N - 1) / W);
+}
+
+// A CTA's walk over its range, one segment (a run of key tiles of one item) at
+// a time.  Every warp role walks on its own; all lanes of a warp take part.
+template <int KT>
+struct AttnWalk {
+  const PagedAttnArgs& a;
+  const long long* pre;
+  long long W, u, u_end;  // units: all, position, end of the range
+  int c, N;
+  // the current segment
+  AttnReq q;
+  int r, h, t;
+  int kbeg, kend;         // key tiles of the segment
+  int k0, k1;             // key tiles of its item
+  bool first;             // the CTA's first segment
+
+  __device__ AttnWalk(const PagedAttnArgs& a_, const long long* pre_) : a(a_), pre(pre_) {
+    c = blockIdx.x;
+    W = pre[a.batch - 1];
+    N = (int)min((long long)gridDim.x, W);  // every range has at least one unit
+    first = true;
+    u = u_end = 0;
+    if (c >= N) return;
+    u = W * c / N;
+    u_end = W * (c + 1) / N;
+    // the request: first r with pre[r] > u
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] > u) hi = mid; else lo = mid + 1;
+    }
+    r = lo;
+    attn_req(a, r, q);
+    const long long base = r ? pre[r - 1] : 0;
+    const long long per = (pre[r] - base) / a.nkv;
+    h = (int)((u - base) / per);
+    long long rem = (u - base) - h * per;
+    // the item tile: 32 at a time
+    const int lane = threadIdx.x & 31, nt = attn_tiles(a, q.n);
+    for (int t0 = 0;; t0 += 32) {
+      int b0 = 0, b1 = 0;
+      if (t0 + lane < nt) tile_range<KT>(a, q, t0 + lane, b0, b1);
+      long long v = b1 - b0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += w;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, v > rem);
+      if (past == 0 && t0 + 32 < nt) {
+        rem -= __shfl_sync(0xffffffffu, v, 31);
+        continue;
+      }
+      const int l = past ? __ffs(past) - 1 : 31;
+      t = t0 + l;
+      rem -= __shfl_sync(0xffffffffu, v - (b1 - b0), l);
+      break;
+    }
+    set_item((int)rem);
+  }
+  __device__ bool done() const { return u >= u_end; }
+  __device__ void set_item(int skip) {
+    tile_range<KT>(a, q, t, k0, k1);
+    kbeg = k0 + skip;
+    kend = (int)min((long long)k1, kbeg + (u_end - u));
+  }
+  __device__ void next() {
+    u += kend - kbeg;
+    first = false;
+    if (u >= u_end) return;
+    int nt = attn_tiles(a, q.n);
+    do {
+      if (++t >= nt) {
+        t = 0;
+        if (++h >= a.nkv) {
+          h = 0;
+          do ++r; while (pre[r] == pre[r - 1]);
+          attn_req(a, r, q);
+          nt = attn_tiles(a, q.n);
+        }
+      }
+      set_item(0);
+    } while (k1 == k0);
+  }
+  __device__ bool whole() const { return kbeg == k0 && kend == k1; }
+  // the CTAs that share the item, and the partial slot of CTA x among them:
+  // 2 x for its first segment, 2 x + 1 for a later one
+  __device__ long long item_begin() const { return u - (kbeg - k0); }
+  __device__ int cta_first() const { return cta_of_unit(item_begin(), W, N); }
+  __device__ int cta_last() const { return cta_of_unit(item_begin() + (k1 - k0) - 1, W, N); }
+  __device__ int slot() const { return 2 * c + (first ? 0 : 1); }
+  // 1 when the item is not the first segment of CTA c0 = cta_first()
+  __device__ int later_in(int c0) const { return item_begin() != W * c0 / N ? 1 : 0; }
+  __device__ int tokens() const { return min(a.ipt, q.n - t * a.ipt); }
+};
+
+// The accumulators of one row over its visible keys of key tiles [kbeg, kend),
+// straight from the pools: out[HD / 32 values a lane, values lane * (HD / 32)..].
+// The tensor-core pass multiplies a masked key's weight, exactly 0, with its
+// value row; where that row holds an infinity or NaN the product poisons rows
+// that do not see the key.  Returns false when no such row exists (then a
+// non-finite result is the row's own).  Called by a warp for a row whose
+// result is not finite, which only such inputs cause.  m: the row's reference
+// maximum in log2 units.  Stops once every column is NaN.
+template <typename T, int HD, int KT>
+__device__ __noinline__ bool masked_key_fallback(const PagedAttnArgs& a, int r, int h,
+                                                 const AttnReq& q, int kbeg, int kend, int i,
+                                                 int g, float m, int lane, float* out) {
+  constexpr int V = HD / 32;
+  const int p = q.st + i;
+  const int from = kbeg * KT, to = min(kend * KT, q.len);
+  const int lo = max(from, row_lo(a, p)), hi = min(to, row_hi(a, q, p));
+  const int32_t* tab = a.table + (int64_t)r * a.max_pages;
+  auto row_at = [&](const void* pool, int key) -> const T* {
+    const int e = tab[key / a.page];
+    if (e < 0 || e >= a.n_pages) return nullptr;  // not visible: the tile held zeros there
+    return static_cast<const T*>(pool) +
+           (((int64_t)e * a.nkv + h) * a.page + key % a.page) * HD + lane * V;
+  };
+  bool found = false;
+  for (int key = from; key < to && !found; ++key) {
+    if (key == lo && hi > lo) key = hi;  // the keys it sees are not the question
+    if (key >= to) break;
+    const T* v = row_at(a.v_pool, key);
+    bool odd = false;
+    if (v != nullptr)
+#pragma unroll
+      for (int d = 0; d < V; ++d) odd |= !isfinite(to_f(v[d]));
+    found = __any_sync(0xffffffffu, odd);
+  }
+  if (!found) return false;
+  const T* qr = static_cast<const T*>(a.q) + (int64_t)(q.row0 + i) * a.q_stride +
+                (int64_t)(h * a.G + g) * HD + lane * V;
+#pragma unroll
+  for (int d = 0; d < V; ++d) out[d] = 0.f;
+  for (int key = lo; key < hi; ++key) {
+    const T* k = row_at(a.k_pool, key);
+    if (k == nullptr) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int d = 0; d < V; ++d) s += to_f(qr[d]) * to_f(k[d]);
+    s = warp_sum(s);
+    // the weight as the tensor cores would have taken it: rounded to T
+    const float w = to_f(from_f<T>(ex2_ftz(fmaf(s, a.scale_log2, -m))));
+    const T* v = row_at(a.v_pool, key);
+    bool alive = false;
+#pragma unroll
+    for (int d = 0; d < V; ++d) {
+      out[d] += w * to_f(v[d]);
+      alive |= !isnan(out[d]);
+    }
+    if (!__any_sync(0xffffffffu, alive)) break;
+  }
+  return true;
+}
+
+}  // namespace dflash

@@ -1,0 +1,308 @@
+// Row operators in front of a paged attention call: per-head RMSNorm with the
+// rotate-half position rotation (queries and keys), and the append of a
+// chunk's keys (normalised, rotated) and values to a paged K/V cache.
+//
+//   norm(x)    = x * rsqrt(mean(x^2) + eps) * g            (g null: x unchanged)
+//   rope(y, p) = (a cos - b sin, b cos + a sin), y = (a, b) in halves, cos and
+//                sin the table rows of position p          (no table: y unchanged)
+//
+// A head row is held by head_dim / 16 lanes, a lane with 8 consecutive values
+// of each half, so a rotation pair never leaves its thread, the norm's sum
+// takes 2 or 3 shuffles, and every global access is 16 bytes.  A group of
+// lanes stays on one row and walks over its heads (kUnroll of them in flight), so
+// the table row sits in registers.  Sums and products are fp32; each value is
+// rounded once, when it is stored.  Bound by memory: every value is read once
+// and written once.
+#include "common.cuh"
+#include "internal.h"
+
+namespace dflash {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // heads a lane group has in flight
+
+// 8 elements as raw 16-byte words, loaded now and converted later.
+template <typename T> struct Raw8 {
+  uint4 w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const T* h = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f(h[i]);
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// Rounds and stores 8 values; true when one does not fit the element type.
+template <typename T>
+__device__ __forceinline__ bool put8(T* dst, const float (&v)[8]) {
+  T h[8];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = from_f<T>(v[i]);
+    bad |= narrow_bad<T>(v[i]);
+  }
+  *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(h);
+  return bad;
+}
+template <>
+__device__ __forceinline__ bool put8<float>(float* dst, const float (&v)[8]) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  return false;
+}
+
+// What a warp learns about a row: its request's rows and first position.
+struct RowOwner {
+  int req, row0, n, st;
+  int total;  // cu_rows[batch]
+};
+
+// The request that holds `row` (the last one whose first row is <= row), by a
+// search over 32 probes a round: one round up to 32 requests, two up to 1024.
+__device__ __forceinline__ RowOwner find_owner(const int32_t* cu, const int32_t* start, int batch,
+                                               int row, int lane) {
+  RowOwner o;
+  if (batch <= 32) {
+    const int l = min(lane, batch - 1);
+    const int a = cu[l], b = cu[l + 1], st = start[l];
+    const unsigned le = __ballot_sync(0xffffffffu, lane < batch && a <= row);
+    o.req = le ? 31 - __clz(le) : 0;
+    o.row0 = __shfl_sync(0xffffffffu, a, o.req);
+    o.n = __shfl_sync(0xffffffffu, b, o.req) - o.row0;
+    o.st = __shfl_sync(0xffffffffu, st, o.req);
+    o.total = __shfl_sync(0xffffffffu, b, batch - 1);
+    return o;
+  }
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < n && cu[lo + min(i, n - 1)] <= row);
+    const int k = le ? 31 - __clz(le) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  o.req = lo;
+  o.row0 = cu[lo];
+  o.n = cu[lo + 1] - o.row0;
+  o.st = start[lo];
+  o.total = cu[batch];
+  return o;
+}
+
+struct RowArgs {
+  const void *a, *b;          // [n_rows][heads][HD], row strides in elements
+  int64_t a_stride, b_stride;
+  const void *g_a, *g_b;      // [HD] of the inputs' type, or null: no norm
+  float eps;
+  const float* rope;          // [2][max_pos][HD / 2] cos then sin, or null
+  int max_pos;
+  const int32_t *cu, *start;
+  int batch, n_rows, n_a, n_b;
+  int groups_log2;            // lane groups per row
+  void *oa, *ob;              // dense rows (kPaged false): row strides oa_stride, ob_stride
+  int64_t oa_stride, ob_stride;
+  const int32_t* table;       // paged (kPaged true): oa = K pool, ob = V pool
+  int max_pages, page, n_pages;
+  int32_t* err;
+};
+
+// kPaged false: a = queries, b = keys, both normalised and rotated into dense
+// rows.  kPaged true: a = keys (normalised, rotated), b = values (copied), into
+// the pages of [n_pages][heads][page][HD] pools.
+template <typename TI, typename TO, int HD, bool kPaged>
+__global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowArgs p) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kLanes = HD / 16, kHalf = HD / 2;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int grp = tid / kLanes, i0 = (tid % kLanes) * 8;
+  const int gpr = 1 << p.groups_log2;  // at least 8, so that a warp's groups share their row
+  const int row = blockIdx.x * ((kThreads / kLanes) >> p.groups_log2) + (grp >> p.groups_log2);
+  if (row >= p.n_rows) return;
+  const int hg = grp & (gpr - 1);
+  const int nh = p.n_a + p.n_b;
+
+  Raw8<TI> x[kUnroll][2];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u * gpr;
+      if (h < nh) {
+        const TI* src = h < p.n_a
+            ? static_cast<const TI*>(p.a) + (int64_t)row * p.a_stride + (int64_t)h * HD
+            : static_cast<const TI*>(p.b) + (int64_t)row * p.b_stride + (int64_t)(h - p.n_a) * HD;
+        x[u][0].load(src + i0);
+        x[u][1].load(src + i0 + kHalf);
+      }
+    }
+  };
+  fetch(hg);  // in flight while the row's request is looked up
+
+  const RowOwner o = find_owner(p.cu, p.start, p.batch, row, lane);
+  if (row >= o.total && o.total >= 0) return;  // padding behind the last request
+  if (row < o.row0 || row - o.row0 >= o.n || o.row0 < 0 || o.row0 + (int64_t)o.n > p.n_rows) {
+    if (lane == 0) set_error(p.err, DFLASH_DEV_ROWS);
+    return;
+  }
+  // the whole request has to fit the table and the cache, else none of its rows is written
+  const int64_t last = (int64_t)o.st + o.n - 1;
+  int64_t cap = p.rope ? p.max_pos : INT64_MAX;
+  if (kPaged) cap = min(cap, (int64_t)p.max_pages * p.page);
+  if (o.st < 0 || last >= cap) {
+    if (lane == 0) set_error(p.err, DFLASH_DEV_CTX_CAP);
+    return;
+  }
+  const int pos = o.st + (row - o.row0);
+  float cs[8], sn[8];
+  if (p.rope) {
+    const float* t = p.rope + (int64_t)pos * kHalf + i0;
+    Raw8<float> c, s;
+    c.load(t);
+    s.load(t + (int64_t)p.max_pos * kHalf);
+    c.get(cs);
+    s.get(sn);
+  }
+  int64_t slot = 0;  // paged: pool row of head 0
+  if (kPaged) {
+    const int32_t* tab = p.table + (int64_t)o.req * p.max_pages;
+    bool bad = false;
+    for (int k = o.st / p.page + lane; k <= (int)(last / p.page); k += 32) {
+      const int e = tab[k];
+      bad |= e < 0 || e >= p.n_pages;
+    }
+    const int e = tab[pos / p.page];
+    if (__any_sync(0xffffffffu, bad)) {
+      if (lane == 0) set_error(p.err, DFLASH_DEV_PAGE);
+      return;
+    }
+    slot = (int64_t)e * p.n_a * p.page + pos % p.page;
+  }
+
+  bool bad = false;
+  for (int h0 = hg;;) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u * gpr;
+      // every lane of the warp takes the shuffles; h is uniform over a group's lanes
+      const bool live = h < nh, is_a = h < p.n_a;
+      float y1[8], y2[8];
+      if (live) {
+        x[u][0].get(y1);
+        x[u][1].get(y2);
+      }
+      const TI* g = static_cast<const TI*>(is_a ? p.g_a : p.g_b);
+      if (p.g_a != nullptr || p.g_b != nullptr) {
+        float ss = 0.f;
+        if (live)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss += y1[i] * y1[i] + y2[i] * y2[i];
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+        if (live && g != nullptr) {
+          const float inv = rsqrtf(ss / HD + p.eps);
+          Raw8<TI> gr;
+          float gv[8];
+          gr.load(g + i0);
+          gr.get(gv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y1[i] = y1[i] * inv * gv[i];
+          gr.load(g + i0 + kHalf);
+          gr.get(gv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y2[i] = y2[i] * inv * gv[i];
+        }
+      }
+      if (!live) continue;
+      if (p.rope && (is_a || !kPaged)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = y1[i], b = y2[i];
+          y1[i] = a * cs[i] - b * sn[i];
+          y2[i] = b * cs[i] + a * sn[i];
+        }
+      }
+      TO* dst;
+      if (kPaged) {
+        const int64_t d = slot + (int64_t)(is_a ? h : h - p.n_a) * p.page;
+        if (!DFLASH_CHECK(d >= 0 && d < (int64_t)p.n_pages * p.n_a * p.page, p.err)) continue;
+        dst = static_cast<TO*>(is_a ? p.oa : p.ob) + d * HD;
+      } else {
+        dst = is_a ? static_cast<TO*>(p.oa) + (int64_t)row * p.oa_stride + (int64_t)h * HD
+                   : static_cast<TO*>(p.ob) + (int64_t)row * p.ob_stride +
+                         (int64_t)(h - p.n_a) * HD;
+      }
+      bad |= put8<TO>(dst + i0, y1) | put8<TO>(dst + i0 + kHalf, y2);
+    }
+    // uniform over the warp: its groups' first heads differ by less than gpr
+    h0 += kUnroll * gpr;
+    if (h0 - hg >= nh) break;
+    fetch(h0);
+  }
+  if (bad) set_error(p.err, DFLASH_DEV_RANGE);
+}
+
+template <typename TI, typename TO, bool kPaged>
+int launch_rows(const RowArgs& a0, int hd, cudaStream_t s) {
+  RowArgs a = a0;
+  const int groups = kThreads / (hd / 16);
+  // Few rows: a CTA per row, so that a row's heads run side by side.  Many
+  // rows: 8 groups a row, which then keep the table row over several heads.
+  a.groups_log2 = a.n_rows <= 8 * num_sms() ? (hd == 128 ? 5 : 6) : 3;
+  const int rows = groups >> a.groups_log2;
+  const dim3 grid((a.n_rows + rows - 1) / rows);
+  TimedScope ts(s, TC_ROW);
+  const cudaError_t e =
+      hd == 128 ? launch_pdl(attn_rows_kernel<TI, TO, 128, kPaged>, grid, dim3(kThreads), 0, s, 1, a)
+                : launch_pdl(attn_rows_kernel<TI, TO, 64, kPaged>, grid, dim3(kThreads), 0, s, 1, a);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ECUDA;
+}
+
+}  // namespace
+
+int launch_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        int dtype, const void* g_q, const void* g_k, float eps, const float* rope,
+                        int max_pos, const int32_t* cu, const int32_t* start, int batch,
+                        int n_rows, int n_q, int n_kv, int hd, void* q_out, int64_t q_out_stride,
+                        void* k_out, int64_t k_out_stride, int32_t* err, cudaStream_t s) {
+  RowArgs a = {q, k, q_stride, k_stride, g_q, g_k, eps, rope, max_pos, cu, start, batch, n_rows,
+               n_q, n_kv, 0, q_out, k_out, q_out_stride, k_out_stride, nullptr, 0, 0, 0, err};
+  if (dtype == DFLASH_BF16) return launch_rows<__nv_bfloat16, __nv_bfloat16, false>(a, hd, s);
+  if (dtype == DFLASH_F16) return launch_rows<__half, __half, false>(a, hd, s);
+  return launch_rows<float, float, false>(a, hd, s);
+}
+
+int launch_kv_append_paged(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           int dtype, const void* g_k, float eps, const float* rope, int max_pos,
+                           const int32_t* cu, const int32_t* start, int batch, int n_rows,
+                           int n_kv, int hd, void* k_pool, void* v_pool, int cache_dtype,
+                           const KvPages& pg, int32_t* err, cudaStream_t s) {
+  RowArgs a = {k, v, k_stride, v_stride, g_k, nullptr, eps, rope, max_pos, cu, start, batch,
+               n_rows, n_kv, n_kv, 0, k_pool, v_pool, 0, 0, pg.table, pg.max_pages, pg.page,
+               pg.n_pages, err};
+  const bool b = cache_dtype == DFLASH_BF16;
+  if (dtype == DFLASH_BF16)
+    return b ? launch_rows<__nv_bfloat16, __nv_bfloat16, true>(a, hd, s)
+             : launch_rows<__nv_bfloat16, __half, true>(a, hd, s);
+  if (dtype == DFLASH_F16)
+    return b ? launch_rows<__half, __nv_bfloat16, true>(a, hd, s)
+             : launch_rows<__half, __half, true>(a, hd, s);
+  return b ? launch_rows<float, __nv_bfloat16, true>(a, hd, s)
+           : launch_rows<float, __half, true>(a, hd, s);
+}
+
+}  // namespace dflash

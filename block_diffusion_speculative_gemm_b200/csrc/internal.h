@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 #include <vector>
 
@@ -44,6 +45,31 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 
 // Streaming multiprocessors of the current device (cached per device).
 int num_sms();
+
+// A kernel's dynamic shared memory limit, raised once per device.
+struct SmemLimit {
+  std::atomic<bool> done[64] = {};
+  bool raise(const void* kernel, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && done[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+      return false;
+    if (known) done[dev].store(true, std::memory_order_release);
+    return true;
+  }
+};
+
+// Workspace header: the device error word (byte 0), then 32768 completion
+// counters: verify uses one per request, the draft attention one per
+// (request, kv head), the paged chunk attention one per CTA.  No call writes the
+// header except through those words, every call leaves the counters it used at
+// zero (calls sharing a workspace never overlap), and each call's own buffers
+// start after the header.
+constexpr size_t kCntOff = 256;
+constexpr size_t kHeader = kCntOff + (size_t(128) << 10);
 
 // ---------------------------------------------------------------- timing
 enum TimingClass { TC_GEMM = 0, TC_ATTN = 1, TC_ROW = 2, TC_VERIFY = 3, TC_LMHEAD = 4, TC_N = 5 };
@@ -284,6 +310,23 @@ int launch_attn_tc(const __half* q, const __half* kb, const __half* vb, const __
                    int hd, int L, int chunk, const int32_t* plan_dev, int n_chunks,
                    const int32_t* seg_start, float* part_o, float* part_ml, unsigned* cnt,
                    __half* o, int32_t* err, cudaStream_t s);
+
+// ---------------------------------------------------------------- paged chunk attention
+// Row operators (attn_rows.cu) and the attention over paged K/V (attn_paged.cu,
+// attn_paged.cuh); strides in elements, arguments as in dflash.h.
+int launch_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        int dtype, const void* g_q, const void* g_k, float eps, const float* rope,
+                        int max_pos, const int32_t* cu, const int32_t* start, int batch,
+                        int n_rows, int n_q, int n_kv, int hd, void* q_out, int64_t q_out_stride,
+                        void* k_out, int64_t k_out_stride, int32_t* err, cudaStream_t s);
+int launch_kv_append_paged(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           int dtype, const void* g_k, float eps, const float* rope, int max_pos,
+                           const int32_t* cu, const int32_t* start, int batch, int n_rows,
+                           int n_kv, int hd, void* k_pool, void* v_pool, int cache_dtype,
+                           const KvPages& pg, int32_t* err, cudaStream_t s);
+struct PagedAttnArgs;
+int attn_paged_ctas();  // CTAs of the few-row kernel's grid
+int launch_attn_paged(const PagedAttnArgs& a, int hd, int dtype, cudaStream_t s);
 
 // T: type of q, the block's k/v and the output o; TC: K/V cache type.
 // Paged K/V (pages.table set) and the persistent schedule (seg_start set) are

@@ -24,6 +24,10 @@
  *                       paged K/V store with prefix sharing.
  *   dflash_draft_begin .. dflash_draft_end, dflash_verify_shard/_merge
  *                       drafting and verify with the vocabulary split over GPUs.
+ *   dflash_qk_norm_rope, dflash_kv_append_paged, dflash_attention_paged
+ *                       the attention part of the target model's own forward
+ *                       (prompts, single tokens, the verify pass over a drafted
+ *                       block) over a paged K/V store of the same layout.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -80,7 +84,7 @@ extern "C" {
 /* ---- element types ---------------------------------------------------- */
 #define DFLASH_F32  0
 #define DFLASH_BF16 1
-#define DFLASH_F16  2  /* operand type of the test hooks in dflash_debug.h only */
+#define DFLASH_F16  2  /* not a model type: paged attention operands and caches, test hooks */
 
 typedef struct dflash_model dflash_model; /* opaque */
 
@@ -431,6 +435,108 @@ int dflash_verify_noalloc(const void* target_logits, int logits_dtype,
                           int32_t* out_tokens, int32_t* out_len, int out_cap, int32_t* seq_lens,
                           int32_t* accept_len, int32_t* next_anchor, int32_t* error_bits,
                           void* stream);
+
+/*
+ * Attention of the target model over paged K/V.  Between dflash_draft_block and
+ * dflash_verify the target scores the drafted block ("DFlash + Spec V2 深度解析",
+ * §2.3, and blog "DFlash：用“块扩散”魔法", §2 Flash Verification: one forward over
+ * the block); its attention layers run these calls in turn on the rows of their
+ * fused QKV projection:
+ *   dflash_qk_norm_rope     RMSNorm of every query and key head, then rotation;
+ *   dflash_kv_append_paged  the same norm and rotation of the keys on their way
+ *                           into the cache, with the values;
+ *   dflash_attention_paged  softmax(scale q k^T) v of each request's new rows over
+ *                           its cache.
+ * The same calls serve prompts (a request's rows are its prompt or a chunk of
+ * it), single-token decoding (one row a request) and mixed batches.
+ *
+ * Shared by the calls:
+ *   rows         [n_rows][heads][head_dim] operands; heads are contiguous, rows are
+ *                `*_stride` elements apart (views into a fused projection), pointers
+ *                and strides multiples of 16 bytes.  head_dim 64 or 128
+ *                (DFLASH_EUNSUPPORTED otherwise).
+ *   cu_rows      device int32 [batch+1], cu_rows[0] = 0, ascending: request r has the
+ *                rows cu_rows[r] .. cu_rows[r+1]-1, possibly none.  Rows from
+ *                cu_rows[batch] up to n_rows are padding: nothing of theirs is
+ *                written.  A request whose rows are not an ascending range inside
+ *                [0, n_rows] writes nothing and sets DFLASH_DEV_ROWS.
+ *   start_pos    device int32 [batch]: position of request r's first row.
+ *   rope         device fp32 [2][max_pos][head_dim/2], the cosines then the sines of
+ *                every position's angles (dflash_rope_table, or a caller's own, for
+ *                scaled rotations), 16-byte aligned, or NULL: no rotation.  Value i
+ *                of a head rotates with value i + head_dim/2.
+ *   g_q, g_k     [head_dim] norm gains of the operands' type, 16-byte aligned, or NULL:
+ *                that operand is not normalised.
+ *   k_pool, v_pool  device [n_pages][n_kv][page_size][head_dim] of one layer, fp16
+ *                (DFLASH_F16) or bf16 (DFLASH_BF16), 16-byte aligned; page_table
+ *                [batch][max_pages] as for dflash_inject_kv_paged.  page_size is 16, 32
+ *                or a multiple of 64; n_pages * n_kv * page_size < 2^31,
+ *                max_pages * page_size <= 2^30 (DFLASH_EUNSUPPORTED otherwise).
+ *   ws           a workspace of at least dflash_attention_paged_workspace_size bytes
+ *                (the first two calls need the header alone: that size for n_rows 0),
+ *                zero-filled once as every workspace.
+ * Arithmetic is fp32, rounded once on the way out (attention's softmax weights also
+ * once, to the operands' type, in front of the second product).  An fp16 result
+ * that overflows sets DFLASH_DEV_RANGE.  A request with a page in use unmapped
+ * writes nothing and sets DFLASH_DEV_PAGE; one whose rows leave the rotation
+ * table or the cache writes nothing and sets DFLASH_DEV_CTX_CAP; the others are
+ * not affected.  After DFLASH_DEV_TIMEOUT zero-fill the workspace again.
+ */
+
+/* Fills a rotation table: cos and sin of p * base^(-2i/head_dim) for p < max_pos,
+ * i < head_dim/2, evaluated in double precision.  Asynchronous on `stream`. */
+int dflash_rope_table(float* table, int max_pos, int head_dim, double base, void* stream);
+
+/* q_out = rope(norm(q; g_q)), k_out = rope(norm(k; g_k)), norm(x; g) =
+ * x / sqrt(mean(x^2) + eps) * g per head.  dtype: DFLASH_F32, DFLASH_BF16 or
+ * DFLASH_F16, of operands, gains and results alike.  q_out = q and k_out = k (same
+ * stride) work in place; other overlaps do not.  n_q = 0 or n_kv = 0 leaves that
+ * operand out (its pointers are not read). */
+int dflash_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        int dtype, const void* g_q, const void* g_k, float eps, const float* rope,
+                        int max_pos, const int32_t* cu_rows, const int32_t* start_pos, int batch,
+                        int n_rows, int n_q, int n_kv, int head_dim, void* q_out,
+                        int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* For every row at position p of request r: K[page][h][slot] = rope(norm(k; g_k)),
+ * V[page][h][slot] = v with page = page_table[r][p / page_size], slot = p %
+ * page_size.  dtype (k, v, g_k): DFLASH_F32, DFLASH_BF16 or DFLASH_F16;
+ * cache_dtype: DFLASH_BF16 or DFLASH_F16.  No two rows of a call may map to the
+ * same (page, slot).  Other slots are left as they were. */
+int dflash_kv_append_paged(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           int dtype, const void* g_k, float eps, const float* rope, int max_pos,
+                           const int32_t* cu_rows, const int32_t* start_pos, int batch, int n_rows,
+                           int n_kv, int head_dim, void* k_pool, void* v_pool, int cache_dtype,
+                           int n_pages, int page_size, const int32_t* page_table, int max_pages,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of one dflash_attention_paged call (0 for shapes that the
+ * call does not support). */
+size_t dflash_attention_paged_workspace_size(int batch, int n_rows, int n_q, int n_kv,
+                                             int head_dim);
+
+/* out[row][h] = sum_j w_j V[j] / sum_j w_j, w_j = exp(scale q[row][h] . K[j]), over
+ * the keys j that the row sees: j < kv_len[r], with `causal` also j <= p, with
+ * window > 0 also j > p - window (p the row's position; query head h reads kv
+ * head h / (n_q / n_kv)).  A row that sees no key gets out = 0 and lse = -inf.
+ *   dtype    DFLASH_BF16 or DFLASH_F16: type of q, the pools and out
+ *   kv_len   device int32 [batch]: keys stored for request r, at most max_pages *
+ *            page_size; NULL: start_pos[r] + its rows (the chunk appended)
+ *   out      rows of out_stride elements, not overlapping q
+ *   lse      device fp32 [n_rows][n_q] out or NULL: ln sum_j w_j
+ * Keys that no row of a request sees are never used, whatever their slots hold
+ * (NaN included), and their pages need not be mapped; a key that only some rows
+ * see does not reach the others.  scale > 0; n_q / n_kv <= 64, batch <= 4096
+ * (DFLASH_EUNSUPPORTED beyond).  The same inputs give the same bits; how a
+ * request's keys are divided over the GPU depends on the whole batch, so its
+ * rows can change at rounding level when the other requests change. */
+int dflash_attention_paged(const void* q, int64_t q_stride, int dtype, const int32_t* cu_rows,
+                           const int32_t* start_pos, const int32_t* kv_len, int batch, int n_rows,
+                           int n_q, int n_kv, int head_dim, const void* k_pool, const void* v_pool,
+                           int n_pages, int page_size, const int32_t* page_table, int max_pages,
+                           float scale, int causal, int window, void* out, int64_t out_stride,
+                           float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* Waits for `stream`, copies the workspace's device error word to *bits and
  * clears it.  The only call that synchronises with the host. */

@@ -11,3 +11,4 @@ from . import sampled_verify  # noqa: F401
 from . import sampled_draft  # noqa: F401
 from . import paged_kv  # noqa: F401
 from . import vocab_parallel  # noqa: F401
+from . import attention_paged  # noqa: F401
