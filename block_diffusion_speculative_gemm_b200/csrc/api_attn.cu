@@ -53,24 +53,24 @@ int check_pool(const void* k_pool, const void* v_pool, int cache_dtype, int n_kv
 }
 
 // Rows of an item tile: the average request's rows decide.  Any tile is right
-// for any mix of lengths.
+// for any mix of lengths; 256 is the tcgen05 kernel's pair of query tiles.
 int pick_tile_rows(int batch, int n_rows, int G) {
-  const int64_t rows = ((int64_t)n_rows + batch - 1) / batch * G;
-  return std::max(G, rows <= 16 ? 16 : rows <= 32 ? 32 : 64) <= 16
-             ? 16
-             : std::max(G, (int)std::min<int64_t>(rows, 64)) <= 32 ? 32 : 64;
+  const int64_t rows = std::max<int64_t>(((int64_t)n_rows + batch - 1) / batch * G, G);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
 }
 
 struct AttnLayout {
   int tile_rows;
-  size_t part_o, part_ml, end;
+  size_t join, part_o, part_ml, end;
 };
 
 AttnLayout attn_layout(int batch, int n_rows, int G, int hd) {
   AttnLayout L;
   L.tile_rows = pick_tile_rows(batch, n_rows, G);
-  const size_t rows = (size_t)2 * attn_paged_ctas() * L.tile_rows;
-  L.part_o = kHeader;
+  const int ctas = L.tile_rows == 256 ? attn_paged_umma_ctas() : attn_paged_ctas();
+  const size_t rows = (size_t)2 * ctas * L.tile_rows;
+  L.join = kHeader;
+  L.part_o = (L.join + attn_paged_join_bytes() + 255) & ~size_t(255);
   L.part_ml = L.part_o + rows * hd * 4;
   L.end = (L.part_ml + rows * 8 + 255) & ~size_t(255);
   return L;
@@ -220,12 +220,14 @@ extern "C" int dflash_attention_paged(const void* q, int64_t q_stride, int dtype
   a.out_stride = out_stride;
   a.lse = lse;
   a.tile_rows = L.tile_rows;
-  a.ipt = L.tile_rows / G;
+  a.ipt = L.tile_rows == 256 ? 2 * (128 / G) : L.tile_rows / G;
   a.part_o = reinterpret_cast<float*>(base + L.part_o);
   a.part_ml = reinterpret_cast<float*>(base + L.part_ml);
   a.cnt = reinterpret_cast<unsigned*>(base + kCntOff);
   a.err = err_word(ws);
   a.k_pool = k_pool;
   a.v_pool = v_pool;
+  if (L.tile_rows == 256)
+    return launch_attn_paged_umma(a, head_dim, dtype, base + L.join, (cudaStream_t)stream);
   return launch_attn_paged(a, head_dim, dtype, (cudaStream_t)stream);
 }

@@ -816,6 +816,22 @@ bool encode_2d(CUtensorMap* m, const void* ptr, int64_t rows, int cols, int ld, 
   return r == CUDA_SUCCESS;
 }
 
+bool encode_rows3(CUtensorMap* m, const void* ptr, int64_t rows, int heads, int cols, int64_t ld,
+                  int box_heads, int box_rows, int elem) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)ld * 2};
+  cuuint32_t box[3] = {(cuuint32_t)kTileK, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt =
+      elem == DFLASH_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUresult r = enc(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool set_tiled_weights(WeightMap& w, const void* tiled) {
   auto enc = get_encode();
   if (!enc || !tiled || (reinterpret_cast<uintptr_t>(tiled) & 15) != 0) return false;

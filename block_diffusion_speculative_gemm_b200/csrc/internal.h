@@ -206,6 +206,11 @@ size_t tiled_bytes(int N, int K);
 // fill outside the tensor.
 bool encode_2d(CUtensorMap* m, const void* ptr, int64_t rows, int cols, int ld, int box_rows,
                int elem);
+// 3D tensor map over [rows][heads][cols] 16-bit elements (row stride `ld`
+// elements, heads contiguous) with a box of 64 columns x box_heads x box_rows,
+// 128-byte swizzle, zero fill outside the tensor.
+bool encode_rows3(CUtensorMap* m, const void* ptr, int64_t rows, int heads, int cols, int64_t ld,
+                  int box_heads, int box_rows, int elem);
 
 // Y = X * W^T for X [M, K] of W's element type (given as n_seg K-segments of
 // seg_k columns, each [M, seg_k] with row stride ld_seg elements) and W [N, K].
@@ -327,6 +332,12 @@ int launch_kv_append_paged(const void* k, int64_t k_stride, const void* v, int64
 struct PagedAttnArgs;
 int attn_paged_ctas();  // CTAs of the few-row kernel's grid
 int launch_attn_paged(const PagedAttnArgs& a, int hd, int dtype, cudaStream_t s);
+// The tcgen05 kernel for many rows (attn_paged_umma.cu): items of two 128-row
+// query tiles (a.ipt / 2 tokens each), then the join of its shared items, whose
+// descriptions take attn_paged_join_bytes() of workspace.
+int attn_paged_umma_ctas();
+size_t attn_paged_join_bytes();
+int launch_attn_paged_umma(const PagedAttnArgs& a, int hd, int dtype, void* join, cudaStream_t s);
 
 // T: type of q, the block's k/v and the output o; TC: K/V cache type.
 // Paged K/V (pages.table set) and the persistent schedule (seg_start set) are
