@@ -185,7 +185,7 @@ extern "C" int dflash_attention_paged(const void* q, int64_t q_stride, int dtype
   if (!(scale > 0.f) || !isfinite(scale) || window < 0) return DFLASH_EINVAL;
   if (!elem_size(dtype)) return DFLASH_EINVAL;
   if (dtype == DFLASH_F32 || (head_dim != 64 && head_dim != 128) || n_q / n_kv > 64 ||
-      batch > kAttnMaxBatch)
+      batch > kAttnMaxBatch || n_rows > (1 << 30))
     return DFLASH_EUNSUPPORTED;
   if (n_rows == 0) return DFLASH_OK;
   if (!cu_rows || !start_pos || !rows_ok(q, q_stride, n_q, head_dim, 2) ||
@@ -218,13 +218,18 @@ extern "C" int dflash_attention_paged(const void* q, int64_t q_stride, int dtype
   a.window = window;
   a.out = out;
   a.out_stride = out_stride;
+  a.wide_out = aligned(out, 32) && out_stride % 16 == 0;
   a.lse = lse;
   a.tile_rows = L.tile_rows;
-  a.ipt = L.tile_rows == 256 ? 2 * (128 / G) : L.tile_rows / G;
+  a.ipq = std::min(L.tile_rows, 128) / G;
+  a.ipt = L.tile_rows == 256 ? 2 * a.ipq : a.ipq;
   a.part_o = reinterpret_cast<float*>(base + L.part_o);
   a.part_ml = reinterpret_cast<float*>(base + L.part_ml);
   a.cnt = reinterpret_cast<unsigned*>(base + kCntOff);
   a.err = err_word(ws);
+  a.by_g = FastDiv(G);
+  a.by_ipt = FastDiv(a.ipt);
+  a.by_page = FastDiv(page_size);
   a.k_pool = k_pool;
   a.v_pool = v_pool;
   if (L.tile_rows == 256)

@@ -26,7 +26,7 @@ namespace dflash {
 
 namespace {
 
-constexpr int kKT = 64;                   // keys per tile
+constexpr int kKL = 6, kKT = 1 << kKL;    // keys per tile
 constexpr int kCompute = 128;             // compute threads
 constexpr int kThreads = kCompute + 32;
 constexpr int kSlots = 6;                 // ring slots, each a K or a V tile
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     s_abort = 0;
   }
   pdl_wait();
-  attn_plan<HD, kKT>(a, pre);  // ends with a barrier
+  attn_plan<HD, kKL>(a, pre);  // ends with a barrier
 
   // a bounded wait that also gives up once another warp has given up
   auto wait = [&](uint32_t b, uint32_t parity) -> bool {
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     return true;
   };
   bool ok = true;
-  AttnWalk<kKT> w(a, pre);
+  AttnWalk<kKL> w(a, pre);
   const int rows_all = a.n_pages * a.nkv * a.page;  // a row past the pools: TMA fills zeros
 
   if (warp == 4) {
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int key = w.kbeg * kKT + (b0 + lane) * box;
           int y = rows_all;
           if (key < w.q.len) {
-            const int e = tab[key / a.page];
-            if (e >= 0 && e < a.n_pages) y = (e * a.nkv + w.h) * a.page + key % a.page;
+            const int pg = a.by_page.div(key), e = tab[pg];
+            if (e >= 0 && e < a.n_pages) y = (e * a.nkv + w.h) * a.page + key - pg * a.page;
           }
           if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
           ent = y;
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int j = 0; j < 2; ++j) {
         row[j] = wm * 16 + g8 + 8 * j;
         const int rr = min(row[j], R - 1);
-        tok[j] = tok0 + rr / a.G;
-        hg[j] = rr % a.G;
+        tok[j] = tok0 + a.by_g.div(rr);
+        hg[j] = rr - (tok[j] - tok0) * a.G;
         lo[j] = row_lo(a, w.q.st + tok[j]);
         hi[j] = row_hi(a, w.q, w.q.st + tok[j]);
       }
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const int hh = __shfl_sync(0xffffffffu, hg[j], rr * 4);
               const int pr = __shfl_sync(0xffffffffu, row[j], rr * 4);
               float acc[HD / 32];
-              if (!masked_key_fallback<T, HD, kKT>(a, w.r, w.h, w.q, w.kbeg, w.kend, tk, hh,
+              if (!masked_key_fallback<T, HD>(a, w.r, w.h, w.q, w.kbeg * kKT, w.kend * kKT, tk, hh,
                                                    mr == -INFINITY ? 0.f : mr, lane, acc))
                 continue;
 #pragma unroll
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               s.w += v.w * f;
             }
             const float inv = L == 0.f ? 0.f : 1.f / L;
-            const int tk = tok0 + rr / a.G, hh = w.h * a.G + rr % a.G;
+            const int ti = a.by_g.div(rr), tk = tok0 + ti, hh = w.h * a.G + rr - ti * a.G;
             uint2 u;
             u.x = pack2<T>(s.x * inv, s.y * inv);
             u.y = pack2<T>(s.z * inv, s.w * inv);

@@ -4,7 +4,11 @@
 // A request's rows are its new tokens x the G = n_q / n_kv query heads of a kv
 // head, packed token-major (row i * G + g), so that one pass over a kv head's
 // keys serves all of them.  An item is (request, kv head, tile of `ipt` tokens)
-// and costs as many units as it has key tiles.  The units of all items, in
+// and costs as many units as it has key tiles of 2^KL keys, and a few more for
+// its start and end (kItemUnits, the last units of the item).  The kernels are
+// templates over KL; KL = 0 stands for the tcgen05 kernel's choice by item: 128
+// keys where the item fills both query tiles, 256 where it has one, which then
+// meets two runs of 128 keys at a time.  The units of all items, in
 // order, are cut into one equal range per CTA: every CTA streams the same
 // number of key tiles however ragged the batch is, at most two of its items
 // are shared with other CTAs (its first and its last), and nothing about the
@@ -28,6 +32,23 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Quotients by a number that is known at launch, for dividends below 2^31
+// (Granlund and Montgomery: with 2^s >= d and m = ceil(2^(31+s) / d), n / d is
+// floor(n m / 2^(31+s))).
+struct FastDiv {
+  unsigned m;
+  int s;  // -1: d = 1
+  FastDiv() = default;
+  explicit FastDiv(int d) : m(0), s(-1) {
+    if (d == 1) return;
+    while ((1LL << (s + 1)) < d) ++s;  // s + 1 = ceil(log2 d)
+    m = (unsigned)(((1ULL << (32 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return s < 0 ? n : (int)(__umulhi((unsigned)n, m) >> s);
+  }
+};
+
 struct PagedAttnArgs {
   const void* q;
   int64_t q_stride;
@@ -39,13 +60,16 @@ struct PagedAttnArgs {
   int causal, window;
   void* out;
   int64_t out_stride;
+  int wide_out;      // rows of out start on 32 bytes
   float* lse;        // [n_rows][nq] or null
   int ipt;           // tokens per item
+  int ipq;           // tokens per query tile (tcgen05 kernel: ipt = 2 ipq)
   int tile_rows;     // rows of an item's partial (>= ipt * G)
   float *part_o, *part_ml;  // slot s: [tile_rows][HD] and [tile_rows][2] (max in log2 units, sum)
   unsigned* cnt;     // one zeroed counter per CTA
   int32_t* err;
   const void *k_pool, *v_pool;
+  FastDiv by_g, by_ipt, by_page;  // divisors G, ipt, page
 };
 
 struct AttnReq {
@@ -76,18 +100,39 @@ __device__ __forceinline__ int row_hi(const PagedAttnArgs& a, const AttnReq& q, 
   return a.causal ? min(q.len, p + 1) : q.len;
 }
 
-// Key tiles [k0, k1) of item tile t (empty when no row of it sees a key).
-template <int KT>
-__device__ __forceinline__ void tile_range(const PagedAttnArgs& a, const AttnReq& q, int t, int& k0,
-                                           int& k1) {
+// Item tile t: the keys [lo, hi) its rows see, and the key tiles [k0, k1) that
+// hold them (none when no row of it sees a key).
+struct TileRange {
+  int lo, hi, k0, k1;
+};
+template <int KL>
+__device__ __forceinline__ TileRange tile_range(const PagedAttnArgs& a, const AttnReq& q, int t) {
   const int i0 = t * a.ipt, i1 = min(q.n, i0 + a.ipt);
-  const int lo = row_lo(a, q.st + i0), hi = row_hi(a, q, q.st + i1 - 1);
-  k0 = lo / KT;
-  k1 = hi > lo ? (hi - 1) / KT + 1 : k0;
+  const int kl = KL > 0 ? KL : i1 - i0 > a.ipq ? 7 : 8;
+  TileRange x;
+  x.lo = row_lo(a, q.st + i0);
+  x.hi = row_hi(a, q, q.st + i1 - 1);
+  x.k0 = x.lo >> kl;
+  x.k1 = x.hi > x.lo ? ((x.hi - 1) >> kl) + 1 : x.k0;
+  return x;
+}
+
+// What starting and finishing an item takes, in key tiles: about 4500 cycles
+// against 3200 a tile in the tcgen05 kernel.  An 8192-token prompt, whose first
+// items have one tile and whose last ones 64, has an uneven end without it.
+template <int KL> constexpr int kItemUnits = KL > 0 ? 1 : 1;
+template <int KL> __device__ __forceinline__ int item_units(const TileRange& x) {
+  return x.k1 > x.k0 ? x.k1 - x.k0 + kItemUnits<KL> : 0;
+}
+
+// Quotient of two non-negative numbers, by the short 32-bit division where both fit.
+__device__ __forceinline__ long long quot(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return (unsigned)n / (unsigned)d;
+  return n / d;
 }
 
 __device__ __forceinline__ int attn_tiles(const PagedAttnArgs& a, int n) {
-  return (n + a.ipt - 1) / a.ipt;
+  return a.by_ipt.div(n + a.ipt - 1);
 }
 
 // Rows of item tile t that see no key: output 0, log-sum-exp -inf.  Called by a warp.
@@ -111,9 +156,9 @@ __device__ __forceinline__ bool pages_mapped(const PagedAttnArgs& a, int r, cons
   bool bad = false;
   if (hi > lo) {
     const int32_t* tab = a.table + (int64_t)r * a.max_pages;
-    const int last = (hi - 1) / a.page;
+    const int last = a.by_page.div(hi - 1);
 #pragma unroll 4
-    for (int k = lo / a.page + lane; k <= last; k += 32) {
+    for (int k = a.by_page.div(lo) + lane; k <= last; k += 32) {
       const int e = tab[k];
       bad |= e < 0 || e >= a.n_pages;
     }
@@ -127,7 +172,7 @@ constexpr int kAttnMaxBatch = 4096;
 // Fills pre[r] with the units of requests 0..r (every thread of the CTA; ends
 // with a barrier).  Requests with bad lengths have none and set their error
 // bits; items without keys have none and are written here, by one CTA each.
-template <int HD, int KT>
+template <int HD, int KL>
 __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthr = blockDim.x, nw = nthr >> 5;
@@ -143,10 +188,9 @@ __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
       const int nt = attn_tiles(a, q.n);
       bool empty = false;
       for (int t = 0; t < min(nt, kFew); ++t) {
-        int k0, k1;
-        tile_range<KT>(a, q, t, k0, k1);
-        u += k1 - k0;
-        empty |= k1 == k0;
+        const TileRange x = tile_range<KL>(a, q, t);
+        u += item_units<KL>(x);
+        empty |= x.k1 == x.k0;
       }
       if (nt > kFew || empty) {
         u = -1;
@@ -164,11 +208,14 @@ __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
       const bool mine = (int)(r % gridDim.x) == (int)blockIdx.x;
       long long u = 0;
       for (int t0 = 0; t0 < nt; t0 += 32) {
-        int k0 = 0, k1 = 0;
-        if (t0 + lane < nt) tile_range<KT>(a, q, t0 + lane, k0, k1);
-        u += k1 - k0;
+        int k = 0;
+        if (t0 + lane < nt) {
+          const TileRange x = tile_range<KL>(a, q, t0 + lane);
+          k = item_units<KL>(x);
+        }
+        u += k;
         if (mine) {
-          unsigned e = __ballot_sync(0xffffffffu, t0 + lane < nt && k1 == k0);
+          unsigned e = __ballot_sync(0xffffffffu, t0 + lane < nt && k == 0);
           if (e && !pages_mapped(a, r, q, lane)) e = 0;
           for (; e; e &= e - 1) zero_rows<HD>(a, q, t0 + __ffs(e) - 1, lane);
         }
@@ -198,36 +245,48 @@ __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
   __syncthreads();
 }
 
-// The CTA whose range holds unit u, when W units are cut into N ranges
-// [W c / N, W (c + 1) / N).
-__device__ __forceinline__ int cta_of_unit(long long u, long long W, int N) {
-  return (int)(((u + 1) * N - 1) / W);
-}
+// The division of W units over N CTAs: the first W % N ranges have one unit more
+// than the others.
+struct UnitSplit {
+  long long each, rest;
+  __device__ UnitSplit(long long W, int N) {
+    each = quot(W, N);
+    rest = W - each * N;
+  }
+  __device__ long long begin(int c) const { return each * c + min((long long)c, rest); }
+  __device__ int owner(long long u) const {
+    const long long wide = rest * (each + 1);
+    return u < wide ? (int)quot(u, each + 1) : (int)(rest + quot(u - wide, each));
+  }
+};
 
 // A CTA's walk over its range, one segment (a run of key tiles of one item) at
 // a time.  Every warp role walks on its own; all lanes of a warp take part.
-template <int KT>
+template <int KL>
 struct AttnWalk {
   const PagedAttnArgs& a;
   const long long* pre;
-  long long W, u, u_end;  // units: all, position, end of the range
-  int c, N;
+  long long u, u_end;     // position, end of the range
+  int c;
+  UnitSplit split;
   // the current segment
   AttnReq q;
   int r, h, t;
   int kbeg, kend;         // key tiles of the segment
-  int k0, k1;             // key tiles of its item
-  bool first;             // the CTA's first segment
+  TileRange x;            // its item's keys and key tiles
+  int off, take;          // units of the item before the segment, units of the segment
 
-  __device__ AttnWalk(const PagedAttnArgs& a_, const long long* pre_) : a(a_), pre(pre_) {
+  __device__ static int ranges(const PagedAttnArgs& a, long long W) {
+    return (int)max(1LL, min((long long)gridDim.x, W));  // every range has at least one unit
+  }
+  __device__ AttnWalk(const PagedAttnArgs& a_, const long long* pre_)
+      : a(a_), pre(pre_), split(pre_[a_.batch - 1], ranges(a_, pre_[a_.batch - 1])) {
     c = blockIdx.x;
-    W = pre[a.batch - 1];
-    N = (int)min((long long)gridDim.x, W);  // every range has at least one unit
-    first = true;
+    const long long W = pre[a.batch - 1];
     u = u_end = 0;
-    if (c >= N) return;
-    u = W * c / N;
-    u_end = W * (c + 1) / N;
+    if (c >= W) return;
+    u = split.begin(c);
+    u_end = split.begin(c + 1);
     // the request: first r with pre[r] > u
     int lo = 0, hi = a.batch - 1;
     while (lo < hi) {
@@ -237,15 +296,18 @@ struct AttnWalk {
     r = lo;
     attn_req(a, r, q);
     const long long base = r ? pre[r - 1] : 0;
-    const long long per = (pre[r] - base) / a.nkv;
-    h = (int)((u - base) / per);
+    const long long per = quot(pre[r] - base, a.nkv);
+    h = (int)quot(u - base, per);
     long long rem = (u - base) - h * per;
     // the item tile: 32 at a time
     const int lane = threadIdx.x & 31, nt = attn_tiles(a, q.n);
-    for (int t0 = 0;; t0 += 32) {
-      int b0 = 0, b1 = 0;
-      if (t0 + lane < nt) tile_range<KT>(a, q, t0 + lane, b0, b1);
-      long long v = b1 - b0;
+    t = 0;
+    for (int t0 = 0; nt > 1; t0 += 32) {
+      int k = 0;
+      if (t0 + lane < nt) {
+        k = item_units<KL>(tile_range<KL>(a, q, t0 + lane));
+      }
+      long long v = k;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long w = __shfl_up_sync(0xffffffffu, v, d);
@@ -258,20 +320,23 @@ struct AttnWalk {
       }
       const int l = past ? __ffs(past) - 1 : 31;
       t = t0 + l;
-      rem -= __shfl_sync(0xffffffffu, v - (b1 - b0), l);
+      rem -= __shfl_sync(0xffffffffu, v - k, l);
       break;
     }
     set_item((int)rem);
+    if (kbeg == kend) next();  // the range begins behind the item's last tile
   }
   __device__ bool done() const { return u >= u_end; }
   __device__ void set_item(int skip) {
-    tile_range<KT>(a, q, t, k0, k1);
-    kbeg = k0 + skip;
-    kend = (int)min((long long)k1, kbeg + (u_end - u));
+    x = tile_range<KL>(a, q, t);
+    const int n = x.k1 - x.k0;
+    off = skip;
+    take = (int)min((long long)item_units<KL>(x) - skip, u_end - u);
+    kbeg = x.k0 + min(skip, n);
+    kend = x.k0 + min(skip + take, n);
   }
   __device__ void next() {
-    u += kend - kbeg;
-    first = false;
+    u += take;
     if (u >= u_end) return;
     int nt = attn_tiles(a, q.n);
     do {
@@ -285,35 +350,35 @@ struct AttnWalk {
         }
       }
       set_item(0);
-    } while (k1 == k0);
+    } while (kbeg == kend);
   }
-  __device__ bool whole() const { return kbeg == k0 && kend == k1; }
-  // the CTAs that share the item, and the partial slot of CTA x among them:
-  // 2 x for its first segment, 2 x + 1 for a later one
-  __device__ long long item_begin() const { return u - (kbeg - k0); }
-  __device__ int cta_first() const { return cta_of_unit(item_begin(), W, N); }
-  __device__ int cta_last() const { return cta_of_unit(item_begin() + (k1 - k0) - 1, W, N); }
-  __device__ int slot() const { return 2 * c + (first ? 0 : 1); }
-  // 1 when the item is not the first segment of CTA c0 = cta_first()
-  __device__ int later_in(int c0) const { return item_begin() != W * c0 / N ? 1 : 0; }
+  __device__ bool whole() const { return kbeg == x.k0 && kend == x.k1; }
+  // the CTAs that share the item's tiles, and the partial slot of CTA x among them:
+  // 2 x for what begins its range, 2 x + 1 for a later segment
+  __device__ long long item_begin() const { return u - off; }
+  __device__ int cta_first() const { return split.owner(item_begin()); }
+  __device__ int cta_last() const { return split.owner(item_begin() + (x.k1 - x.k0) - 1); }
+  __device__ int slot() const { return 2 * c + (u != split.begin(c) ? 1 : 0); }
+  // 1 when the item is not what begins the range of CTA c0 = cta_first()
+  __device__ int later_in(int c0) const { return item_begin() != split.begin(c0) ? 1 : 0; }
   __device__ int tokens() const { return min(a.ipt, q.n - t * a.ipt); }
 };
 
-// The accumulators of one row over its visible keys of key tiles [kbeg, kend),
-// straight from the pools: out[HD / 32 values a lane, values lane * (HD / 32)..].
+// The accumulators of one row over its visible keys among [from, to0), straight
+// from the pools: out[HD / 32 values a lane, values lane * (HD / 32)..].
 // The tensor-core pass multiplies a masked key's weight, exactly 0, with its
 // value row; where that row holds an infinity or NaN the product poisons rows
 // that do not see the key.  Returns false when no such row exists (then a
 // non-finite result is the row's own).  Called by a warp for a row whose
 // result is not finite, which only such inputs cause.  m: the row's reference
 // maximum in log2 units.  Stops once every column is NaN.
-template <typename T, int HD, int KT>
+template <typename T, int HD>
 __device__ __noinline__ bool masked_key_fallback(const PagedAttnArgs& a, int r, int h,
-                                                 const AttnReq& q, int kbeg, int kend, int i,
+                                                 const AttnReq& q, int from, int to0, int i,
                                                  int g, float m, int lane, float* out) {
   constexpr int V = HD / 32;
   const int p = q.st + i;
-  const int from = kbeg * KT, to = min(kend * KT, q.len);
+  const int to = min(to0, q.len);
   const int lo = max(from, row_lo(a, p)), hi = min(to, row_hi(a, q, p));
   const int32_t* tab = a.table + (int64_t)r * a.max_pages;
   auto row_at = [&](const void* pool, int key) -> const T* {

@@ -1,27 +1,31 @@
-// Paged chunk attention for many rows per kv head (prompts, long chunks) on
-// the 5th-generation tensor cores: the formulas of attn_paged.cu with a
-// thread per row.
+// Paged chunk attention on the 5th-generation tensor cores: the formulas of
+// attn_paged.cu with a thread per row.
 //
-// An item is two query tiles of 128 rows (tokens x query heads of a kv head)
-// against 128-key tiles.  S = Q K^T (UMMA 128 x 128) lands in TMEM; a softmax
-// thread owns one row, i.e. one TMEM lane, so the row maximum and sum need no
-// exchange; it writes P over the first half of S's columns in the operand
-// type, and O += P V takes P straight from TMEM (A operand) with V as the
-// MN-major B operand.  Per CTA (one per SM):
+// The CTA works on two tiles of S = Q K^T at a time, 128 rows x 128 keys each
+// (UMMA into TMEM).  An item that fills both query tiles meets one run of 128
+// keys with both of them; one that has a single query tile meets two runs of
+// 128 keys, each with its own accumulators, joined at the end of the segment.
+// A softmax thread owns one row of a tile, i.e. one TMEM lane, so the row
+// maximum and sum need no exchange; it writes P over the first half of S's
+// columns in the operand type, and O += P V takes P straight from TMEM (A
+// operand) with V as the MN-major B operand.  Per CTA (one per SM):
 //
-//   warps 0-3, 4-7  softmax of query tile 0 and 1, and their results
+//   warps 0-3, 4-7  softmax of tile 0 and 1, and their results
 //   warp 8          TMA: K and V tiles through one ring of slots, Q per item
-//   warp 9          MMA issue: QK0(j), PV1(j-1), QK1(j), PV0(j), ...
+//   warps 9, 10     the products of tile 0 and 1: S(j), then O += P(j) V
+//   warp 11         the CTA's segments, described ahead of the others' work
 //
-// so the tensor cores work on one query tile while the other one is in its
-// softmax.  S of a tile is overwritten by the next product only after P of it
-// has been read, which the issue order alone guarantees.  O is rescaled in
-// TMEM only when a row's maximum grew by more than 2^8 since its reference was
-// set (weights then stay below 2^8, exact enough in fp32 sums and inside
-// fp16); normalisation happens once, at the end.
+// so the tensor cores work on one tile while the other one is in its softmax.
+// S of a tile is overwritten by the next product only after P of it has been
+// read, which the issue order alone guarantees.   Half of P is handed over while
+// the exponentials of the other half run.  O is rescaled in TMEM
+// only when a row's maximum grew by more than 2^8 since its reference was set
+// (weights then stay below 2^8, exact enough in fp32 sums and inside fp16);
+// normalisation happens once, at the end.
 //
 // Bound by the tensor cores and, equally, by the exponentials: 4 x 128 x 128 x
-// HD flop and 2 x 128 x 128 exponentials per pair of tiles.
+// HD flop and 128 x 128 exponentials a tile, 1024 cycles each at head_dim 128.
+// kPoly of 8 pairs of exponentials are therefore evaluated on the FMA pipe.
 #include <algorithm>
 
 #include "attn_paged.cuh"
@@ -30,12 +34,17 @@ namespace dflash {
 
 namespace {
 
-constexpr int kKT = 128;          // keys per tile
+constexpr int kKT = 128;          // keys per tile of S
 constexpr int kQT = 128;          // rows per query tile
-constexpr int kThreads = 384;     // three warpgroups: softmax 0, softmax 1, TMA + MMA
+constexpr int kSoftmaxWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kPlanWarp = 11;
+constexpr int kThreads = 384;     // the last four warps: a warpgroup of their own
 constexpr int kMaxSlots = 12;
+constexpr int kSegs = 2;          // segments described ahead
+constexpr int kBars = 2 * kMaxSlots + 8 + 3 * kSegs + 3 + 4 + 2;
+constexpr int kPoly = 2;          // of 8 pairs of exponentials, those on the FMA pipe
 constexpr float kLazy = 8.f;      // log2 growth of a row's maximum before O is rescaled
-// registers per thread: 168 at launch; 216 + 216 + 72 = 3 x 168
+// registers per thread: 168 at launch; 2 x 216 + 72 = 3 x 168
 constexpr int kRegSoftmax = 216, kRegOther = 72;
 
 template <int HD> constexpr int tile_bytes() { return kKT * HD * 2; }
@@ -68,15 +77,74 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
   return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's rows are TMEM lanes, two 16-bit values a column.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// The products, issued by the lanes whose `on` is set (one lane) with the whole
+// warp converged: control flow and operands then are uniform over the warp, and
+// the instruction's operands stay in uniform registers.  In a branch of one lane
+// each of the eight instructions of a product took 120 to 170 cycles to issue,
+// more than the 64 that it runs.
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void umma_ss(uint32_t on, uint32_t d_tmem, uint64_t adesc,
+                                        uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are TMEM lanes, two 16-bit values a column.
+__device__ __forceinline__ void umma_ts(uint32_t on, uint32_t d_tmem, uint32_t a_tmem,
+                                        uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar),
+      "r"(on)
+      : "memory");
+}
+// Arrival of the lanes whose `on` is set, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+// 1 in one lane of the warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// A value that all lanes hold alike, as one the compiler knows to be uniform.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// 32 consecutive bytes: one wide store, or two where they may start on 16 bytes.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* u, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
 }
 
 #define R4(a, i) "=f"(a[i]), "=f"(a[i + 1]), "=f"(a[i + 2]), "=f"(a[i + 3])
@@ -84,41 +152,254 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 #define W4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
 #define W16(a, i) W4(a, i), W4(a, i + 4), W4(a, i + 8), W4(a, i + 12)
 
-// 64 consecutive fp32 columns of this thread's TMEM lane into v[base..]; the
-// values are there when it returns.
-template <int BASE, int N>
-__device__ __forceinline__ void tmem_ld64(uint32_t addr, float (&v)[N]) {
+// Consecutive fp32 columns of this thread's TMEM lane; the values are there when
+// it returns.
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,"
-      "%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : R16(v, BASE), R16(v, BASE + 16), R16(v, BASE + 32), R16(v, BASE + 48)
+      : R16(v, 0)
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32f(uint32_t addr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
-      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : R16(v, 0), R16(v, 16)
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R16(v, 0), R16(v, 16), R16(v, 32), R16(v, 48)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[128]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+      "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+      "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R16(v, 0), R16(v, 16), R16(v, 32), R16(v, 48), R16(v, 64), R16(v, 80), R16(v, 96), R16(v, 112)
+      : "r"(addr)
+      : "memory");
+}
+// The same, there after tmem_landed.
+__device__ __forceinline__ void tmem_ld_start(uint32_t addr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : R16(v, 0), R16(v, 16)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      W16(v, 0)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-      "%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
       W16(v, 0), W16(v, 16)
       : "memory");
+}
+// Four pieces asked for before; the empty operands keep their uses behind the wait.
+#define L4(a, i) "+f"(a[i]), "+f"(a[i + 1]), "+f"(a[i + 2]), "+f"(a[i + 3])
+#define L16(a, i) L4(a, i), L4(a, i + 4), L4(a, i + 8), L4(a, i + 12)
+__device__ __forceinline__ void tmem_landed(float (&a)[32], float (&b)[32], float (&c)[32],
+                                            float (&d)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : L16(a, 0), L16(a, 16), L16(b, 0), L16(b, 16), L16(c, 0), L16(c, 16), L16(d, 0),
+                 L16(d, 16)
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+
+// Two fp32 values in one 64-bit register, for the packed FMA pipe.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three; NaN when one is NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 2^x of two values without the special-function unit: x = n + f with n the
+// nearest integer (by adding 1.5 x 2^23) and |f| <= 1/2, a degree-5 polynomial
+// for 2^f (least largest relative error, found by linear programming on a grid:
+// 2e-7 with the coefficients rounded to fp32, as good as ex2_ftz), n added to
+// its exponent.  Values below -125 give about 2^-125, which no fp32 sum next to
+// a weight of 2^-8 or more sees.  NaN does not come through.
+__device__ __forceinline__ void ex2_poly2(uint64_t x, float& r0, float& r1) {
+  float a, b;
+  unpair(x, a, b);
+  x = pair(fmaxf(a, -125.f), fmaxf(b, -125.f));
+  constexpr float kMagic = 12582912.f;
+  const uint64_t t = add2(x, pair(kMagic, kMagic));
+  const uint64_t n = add2(t, pair(-kMagic, -kMagic));
+  const uint64_t f = fma2(n, pair(-1.f, -1.f), x);
+  uint64_t p = fma2(f, pair(0.001327647129073739f, 0.001327647129073739f),
+                    pair(0.009675540961325169f, 0.009675540961325169f));
+  p = fma2(p, f, pair(0.05550713092088699f, 0.05550713092088699f));
+  p = fma2(p, f, pair(0.24022120237350464f, 0.24022120237350464f));
+  p = fma2(p, f, pair(0.6931469440460205f, 0.6931469440460205f));
+  p = fma2(p, f, pair(1.0000001192092896f, 1.0000001192092896f));
+  float p0, p1, t0, t1;
+  unpair(p, p0, p1);
+  unpair(t, t0, t1);
+  r0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  r1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
+// Keys [32 B, 32 B + 32) of a row's scores: weights 2^(c s - ref) rounded to the
+// operand type into u, their unrounded sum into l0 + l1 (pairs).
+template <typename T, bool kFast>
+__device__ __forceinline__ void weights32(const float* s, uint64_t c2, uint64_t nref2,
+                                          uint32_t* u, uint64_t& l0, uint64_t& l1) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t x = fma2(pair(s[2 * i], s[2 * i + 1]), c2, nref2);
+    float e0, e1;
+    if (kFast && (i * kPoly) % 8 < kPoly) {
+      ex2_poly2(x, e0, e1);
+    } else {
+      unpair(x, e0, e1);
+      e0 = ex2_ftz(e0);
+      e1 = ex2_ftz(e1);
+    }
+    const uint64_t e = pair(e0, e1);
+    if (i & 1) l1 = add2(l1, e); else l0 = add2(l0, e);
+    // rounded to the operand type: relative error at most half a step per weight
+    u[i] = pack2<T>(e0, e1);
+  }
+}
+
+// A row's weights, into TMEM columns tS.., and their sum; p_half is told of the
+// first 64 keys' (late enough that nothing waits for the stores), p_full of all.
+// No branch inside, so that the instructions of all 128 keys can overlap.
+template <typename T, bool kFast>
+__device__ __forceinline__ void tile_weights(const float (&s)[4][32], uint64_t c2, uint64_t nref2,
+                                             uint32_t tS, uint32_t on, uint32_t p_half,
+                                             uint32_t p_full, uint64_t& l0, uint64_t& l1) {
+  uint32_t u[4][16];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    weights32<T, kFast>(s[c], c2, nref2, u[c], l0, l1);
+    if (c < 2) tmem_st(tS + c * 16, u[c]);
+    if (c == 2) {
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_if(on, p_half);
+      tmem_st(tS + c * 16, u[c]);
+    }
+    if (c == 3) {
+      tmem_st(tS + c * 16, u[c]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_if(on, p_full);
+    }
+  }
+}
+
+// A segment of the CTA's work, as the planning warp describes it to the others.
+// two: tile x is query tile x against run j of 128 keys, j < runs.  Otherwise
+// tile x is the one query tile against run 2 j + x, the last of which may be
+// missing for x = 1.
+struct Seg {
+  int more;        // 0: the end
+  int two, whole;  // whole: the segment is all of its item
+  int r, h, row0, st, len;
+  int tok0, tokens;
+  int run0, runs;
+  int slot;        // partial slot
+  int mapped;      // the request's pages are (known by seg_info)
+  __device__ int steps(int x) const { return two ? runs : (runs + 1 - x) >> 1; }
+  __device__ int run(int x, int j) const { return run0 + (two ? j : 2 * j + x); }
+};
+
+// Shared memory beside the tiles.
+struct Fixed {
+  float2 row[2][kQT];  // what the two threads of a row exchange
+  uint64_t bars[kBars];
+  Seg seg[kSegs];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Fixed) % 8 == 0, "the units follow");
+
+// Test of an mbarrier's phase that sleeps up to kNapNs until it completes.
+constexpr uint32_t kNapNs = 20000;
+__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kNapNs)
+      : "memory");
+  return ok != 0;
+}
+
+// A position of the ring, by counting: a division by the number of slots would
+// take longer than a product's instructions.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ void next(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -133,59 +414,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kHalfTile = kKT * 128;  // one 64-column half
   constexpr int kHalves = HD / 64;
   constexpr uint32_t kColS = 0, kColO = 256;  // S0, S1 (P over their first halves), O0, O1
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  // Q tiles, the ring, the units of the batch's requests
+  // Q tiles, the ring, the fixed part, the units of the batch's requests
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + 2 * kTile;
-  long long* pre = reinterpret_cast<long long*>(ring + slots * kTile);
-  __shared__ __align__(8) uint64_t bars[2 * kMaxSlots + 9];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  Fixed& fx = *reinterpret_cast<Fixed*>(ring + slots * kTile);
+  long long* pre = reinterpret_cast<long long*>(&fx + 1);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  auto bar = [&](int i) { return smem_u32(&fx.bars[i]); };
   auto full = [&](int s) { return bar(s); };
   auto empty = [&](int s) { return bar(kMaxSlots + s); };
   constexpr int kB = 2 * kMaxSlots;
   auto s_full = [&](int x) { return bar(kB + x); };
-  auto p_full = [&](int x) { return bar(kB + 2 + x); };
-  auto o_full = [&](int x) { return bar(kB + 4 + x); };
-  const uint32_t q_full = bar(kB + 6), q_empty = bar(kB + 7), all_done = bar(kB + 8);
+  auto p_half = [&](int x) { return bar(kB + 2 + x); };
+  auto p_full = [&](int x) { return bar(kB + 4 + x); };
+  auto o_full = [&](int x) { return bar(kB + 6 + x); };
+  auto seg_full = [&](int k) { return bar(kB + 8 + k % kSegs); };
+  auto seg_info = [&](int k) { return bar(kB + 8 + kSegs + k % kSegs); };
+  auto seg_empty = [&](int k) { return bar(kB + 8 + 2 * kSegs + k % kSegs); };
+  const uint32_t q_full = bar(kB + 8 + 3 * kSegs), q_empty = bar(kB + 9 + 3 * kSegs);
+  const uint32_t all_done = bar(kB + 10 + 3 * kSegs);
+  // meetings of the two softmax warps that hold the same rows
+  auto met_rows = [&](int quarter) { return bar(kB + 11 + 3 * kSegs + quarter); };
+  auto s_read = [&](int x) { return bar(kB + 15 + 3 * kSegs + x); };
   if (tid == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      mbar_init(empty(s), 2);  // the warps of both tiles' products
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(s_full(x), 1);
-      mbar_init(p_full(x), 4);  // the query tile's warps
+      mbar_init(p_half(x), 4);  // the tile's warps
+      mbar_init(p_full(x), 4);
       mbar_init(o_full(x), 1);
+      mbar_init(s_read(x), 4);
     }
+    for (int k = 0; k < kSegs; ++k) {
+      mbar_init(seg_full(k), 1);
+      mbar_init(seg_info(k), 1);
+      mbar_init(seg_empty(k), kSoftmaxWarps + 3);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(met_rows(i), 2);
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(all_done, 1);
+    mbar_init(q_empty, 2);
+    mbar_init(all_done, 2);
     fence_barrier_init();
-    s_abort = 0;
+    fx.abort = 0;
   }
-  if (warp == 9) {
-    tmem_alloc(smem_u32(&s_tmem), 512);
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&fx.tmem), 512);
     tmem_relinquish();
   }
   pdl_wait();
   if (tid == 0) join[blockIdx.x].valid = 0;
   tc_fence_before();
-  attn_plan<HD, kKT>(a, pre);  // ends with a barrier
+  attn_plan<HD, 0>(a, pre);  // ends with a barrier
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they start at 0
 
-  // a bounded wait that also gives up once another warp has given up
+  // a bounded wait that also gives up once another warp has given up; a test
+  // that finds the phase incomplete sleeps for a while, so that waiting warps
+  // leave the issue slots to the others
   auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-    if (mbar_try_wait(b, parity)) return true;
+    if (try_wait_for(b, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(b, parity)) {
-      if (*(volatile int*)&s_abort || global_ns() - t0 > kWaitNs) {
-        *(volatile int*)&s_abort = 1;
+    while (!try_wait_for(b, parity)) {
+      if (*(volatile int*)&fx.abort || global_ns() - t0 > kWaitNs) {
+        *(volatile int*)&fx.abort = 1;
         return false;
       }
     }
@@ -194,125 +489,216 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(b, parity));
   };
+  auto phase = [](int k) { return (uint32_t)(k / kSegs) & 1; };
+  // swizzled tiles start on 1024 bytes, as the symbol's alignment asks
   bool ok = true;
-  const int ipq = a.ipt / 2;  // tokens per query tile
+  const bool placed = (smem_u32(smem) & 1023) == 0 && fx.tmem == tmem;
+  if (!placed) ok = false;
   const uint32_t s_q = smem_u32(smem), s_ring = smem_u32(ring);
 
-  if (warp >= 8) {
+  if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == 8) {
+    if (warp == kPlanWarp) {
+      // ---------------------------------------------------------- segments
+      int checked = -1, k = 0;
+      bool mapped = false;
+      if (ok) {
+        AttnWalk<0> w(a, pre);
+        for (;; ++k) {
+          if (k >= kSegs && !wait_warp(seg_empty(k), phase(k - kSegs))) { ok = false; break; }
+          Seg& d = fx.seg[k % kSegs];
+          if (w.done()) {
+            if (lane == 0) {
+              d.more = 0;
+              mbar_arrive(seg_full(k));
+            }
+            break;
+          }
+          const bool two = w.tokens() > a.ipq, whole = w.whole();
+          const int tok0 = w.t * a.ipt, tokens = w.tokens();
+          if (lane == 0) {
+            d.more = 1;
+            d.two = two;
+            d.whole = whole;
+            d.r = w.r;
+            d.h = w.h;
+            d.row0 = w.q.row0;
+            d.st = w.q.st;
+            d.len = w.q.len;
+            d.tok0 = tok0;
+            d.tokens = tokens;
+            d.run0 = two ? w.kbeg : max(w.kbeg * 2, w.x.lo >> 7);
+            d.runs = (two ? w.kend : min(w.kend * 2, ((w.x.hi - 1) >> 7) + 1)) - d.run0;
+            d.slot = w.slot();
+            mbar_arrive(seg_full(k));
+          }
+          __syncwarp();
+          if (w.r != checked) {
+            checked = w.r;
+            mapped = pages_mapped(a, w.r, w.q, lane);
+            if (!mapped && lane == 0) set_error(a.err, DFLASH_DEV_PAGE);
+          }
+          if (lane == 0) {
+            d.mapped = mapped;
+            mbar_arrive(seg_info(k));
+            if (!whole && w.kbeg == w.x.k0) {
+              JoinItem ji;
+              ji.valid = mapped;
+              ji.row0 = w.q.row0;
+              ji.tok0 = tok0;
+              ji.tokens = tokens;
+              ji.h = w.h;
+              ji.last = w.cta_last();
+              ji.late = w.slot() & 1;
+              ji.pad = 0;
+              join[blockIdx.x] = ji;
+            }
+          }
+          w.next();
+        }
+      }
+    } else if (warp == kTmaWarp) {
       // ---------------------------------------------------------- TMA
-      AttnWalk<kKT> w(a, pre);
       const int rows_all = a.n_pages * a.nkv * a.page;  // past the pools: TMA fills zeros
       const int per = kKT / box;
-      int it = 0, seg = 0;
-      for (; !w.done() && ok; w.next(), ++seg) {
-        const int32_t* tab = a.table + (int64_t)w.r * a.max_pages;
+      RingPos at;
+      int it = 0, k = 0;  // tiles asked for, segments
+      for (; ok; ++k) {
+        if (!wait_warp(seg_full(k), phase(k))) { ok = false; break; }
+        const Seg g = fx.seg[k % kSegs];
+        if (!g.more) break;
+        // keys that one query tile reads pass through once
+        const uint64_t pol = g.two ? policy_evict_last() : policy_evict_first();
+        const int32_t* tab = a.table + (int64_t)g.r * a.max_pages;
         int ent = 0, ent_base = -1;
-        for (int kt = w.kbeg; kt < w.kend && ok; ++kt) {
-          // the pool rows of the tile's boxes, looked up 32 boxes at a time
-          const int b0 = (kt - w.kbeg) * per;
-          if (ent_base < 0 || b0 + per > ent_base + 32) {
+        const int quad = g.two ? 1 : 2;  // runs per step
+        for (int j = 0; j < g.runs && ok; j += quad) {
+          // the pool rows of the step's boxes, looked up 32 boxes at a time
+          const int b0 = j * per;
+          if (ent_base < 0 || b0 + quad * per > ent_base + 32) {
             ent_base = b0;
-            const int key = w.kbeg * kKT + (b0 + lane) * box;
+            const int key = g.run0 * kKT + (b0 + lane) * box;
             int y = rows_all;
-            if (key < w.q.len) {
-              const int e = tab[key / a.page];
-              if (e >= 0 && e < a.n_pages) y = (e * a.nkv + w.h) * a.page + key % a.page;
+            if (key < g.len) {
+              const int pg = a.by_page.div(key), e = tab[pg];
+              if (e >= 0 && e < a.n_pages) y = (e * a.nkv + g.h) * a.page + key - pg * a.page;
             }
             if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
             ent = y;
           }
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++it) {
-            const int s = it % slots;
+          const int nr = min(quad, g.runs - j);
+          for (int o = 0; o < 2 * nr; ++o, ++it) {  // K of the step's runs, then V
+            const int kv = o >= nr, run = kv ? o - nr : o;
+            const int s = at.slot;
             if (it >= slots) {
-              ok = wait_warp(empty(s), ((it / slots) - 1) & 1);
+              ok = wait_warp(empty(s), at.phase ^ 1);
               if (!ok) break;
             }
+            at.next(slots);
             if (lane == 0) mbar_arrive_expect_tx(full(s), kTile);
             __syncwarp();
             for (int b = 0; b < per; ++b) {
-              const int y = __shfl_sync(0xffffffffu, ent, b0 + b - ent_base);
+              const int y = __shfl_sync(0xffffffffu, ent, b0 + run * per + b - ent_base);
               if (lane < kHalves)
                 tma_load_2d(s_ring + s * kTile + b * box * 128 + lane * kHalfTile,
-                            kv ? &tmV : &tmK, full(s), lane * 64, y, policy_evict_last());
+                            kv ? &tmV : &tmK, full(s), lane * 64, y, pol);
             }
-            if (kt == w.kbeg && kv == 0) {
+            if (j == 0 && o == 0) {
               // the item's queries, behind its first keys: the last products of the
               // segment before release the buffer
-              if (seg > 0 && !wait_warp(q_empty, (seg - 1) & 1)) {
+              if (k > 0 && !wait_warp(q_empty, (k - 1) & 1)) {
                 ok = false;
+                ++it;  // this slot's copies are in flight
                 break;
               }
               if (lane == 0) {
-                const int nx = w.tokens() > ipq ? 2 : 1;
-                mbar_arrive_expect_tx(q_full, nx * kHalves * ipq * a.G * 128);
+                const int nx = g.two ? 2 : 1;
+                mbar_arrive_expect_tx(q_full, nx * kHalves * a.ipq * a.G * 128);
                 for (int x = 0; x < nx; ++x)
                   for (int hf = 0; hf < kHalves; ++hf)
                     tma_load_3d(s_q + x * kTile + hf * kHalfTile, &tmQ, q_full, hf * 64,
-                                w.h * a.G, w.q.row0 + w.t * a.ipt + x * ipq);
+                                g.h * a.G, g.row0 + g.tok0 + x * a.ipq);
               }
               __syncwarp();
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty(k));
       }
       // the copies in flight land before the CTA may end
       for (int j = max(0, it - slots); j < it; ++j)
         ok &= mbar_wait(full(j % slots), (j / slots) & 1);
-    } else if (warp == 9) {
-      // ---------------------------------------------------------- MMA
-      AttnWalk<kKT> w(a, pre);
+      if (k > 0) ok &= mbar_wait(q_full, (k - 1) & 1);
+    } else {
+      // ---------------------------------------------------------- MMA of tile x
+      const int x = warp - kMmaWarp;
+      const uint32_t on = elect_one();
       const uint32_t id_s = idesc_f16kind(kQT, kKT, kBf16);
       const uint32_t id_o = idesc_f16kind(kQT, HD, kBf16) | (1u << 16);  // B MN-major
-      int it = 0, seg = 0;             // ring position, segments so far
-      int tiles = 0, tiles1 = 0;       // key tiles so far, those of query tile 1
-      auto qk = [&](int x, int slot) {
-        const uint64_t dq = smem_desc_sw128(s_q + x * kTile);
-        const uint64_t dk = smem_desc_sw128(s_ring + slot * kTile);
-#pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          const uint64_t off = (uint64_t)((ks >> 2) * (kHalfTile >> 4) + (ks & 3) * 2);
-          umma_f16(tmem + kColS + x * 128, dq + off, dk + off, id_s, ks > 0 ? 1u : 0u);
-        }
-        umma_commit(s_full(x));
+      const uint32_t t_s = tmem + kColS + x * 128, t_o = tmem + kColO + x * 128;
+      // Both warps visit every ring position in order and release it once, also the
+      // tiles that only the other one multiplies with.
+      RingPos at;
+      int done = 0;       // tiles so far
+      int other = 0;      // of the other tile
+      bool turn = false;  // tile 0: the step before had a tile 1
+      auto pass = [&]() -> bool {
+        if (!wait_warp(full(at.slot), at.phase)) return false;
+        if (lane == 0) mbar_arrive(empty(at.slot));
+        at.next(slots);
+        return true;
       };
-      auto pv = [&](int x, int slot, bool first) {
-        const uint64_t dv = desc_mn(s_ring + slot * kTile, kHalfTile);
-#pragma unroll
-        for (int ks = 0; ks < kKT / 16; ++ks)
-          umma_f16_ts(tmem + kColO + x * 128, tmem + kColS + x * 128 + ks * 8,
-                      dv + (uint64_t)(ks * 128), id_o, (!first || ks > 0) ? 1u : 0u);
+      // The tiles take turns: a tile's next scores start when the other one's threads
+      // have their maxima, so that one is in its exponentials while the products of
+      // the other run.  Left alone they fall into step, and wait for the
+      // special-function unit and for the products together.  Tile 1 waits in every
+      // step of tile 0, tile 0 after every step of tile 1, so that neither passes
+      // over a phase.
+      auto take_turn = [&]() -> bool {
+        return x == 0 && !turn ? true : wait_warp(s_read(x ^ 1), (other - 1 + x) & 1);
       };
-      for (; !w.done() && ok; w.next(), ++seg) {
-        const bool two = w.tokens() > ipq;
-        const int n = w.kend - w.kbeg;
-        if (!wait_warp(q_full, seg & 1)) { ok = false; break; }
-        for (int j = 0; j < n; ++j, ++tiles) {
-          const int sk = (it + 2 * j) % slots, sv = (it + 2 * j + 1) % slots;
-          if (!wait_warp(full(sk), ((it + 2 * j) / slots) & 1)) { ok = false; break; }
+      for (int k = 0; ok; ++k) {
+        if (!wait_warp(seg_full(k), phase(k))) { ok = false; break; }
+        const Seg& g = fx.seg[k % kSegs];
+        if (!uniform(g.more)) break;
+        const bool two = uniform(g.two);
+        const int n = uniform(g.steps(x)), n0 = uniform(g.steps(0)), n1 = uniform(g.steps(1));
+        const int run0 = uniform(g.run0), len = uniform(g.len);
+        const uint64_t dq = smem_desc_sw128(s_q + (two ? x : 0) * kTile);
+        if (!wait_warp(q_full, k & 1)) { ok = false; break; }
+        if (n == 0 && lane == 0) mbar_arrive(q_empty);
+        int sk = 0;  // slot of the step's K tile
+        auto k_ready = [&]() -> bool {
+          if (x == 1 && !two && !pass()) return false;
+          if (!wait_warp(full(at.slot), at.phase)) return false;
+          sk = at.slot;
+          at.next(slots);
+          return take_turn();
+        };
+        if (n > 0 && !(ok = k_ready())) break;
+        for (int j = 0; j < n; ++j, ++done) {
+          const bool both = j < n1;  // both tiles take part
           tc_fence_after();
-          if (lane == 0) qk(0, sk);
-          if (two && j > 0) {
-            if (!wait_warp(p_full(1), (tiles1++) & 1)) { ok = false; break; }
-            tc_fence_after();
-            const int sp = (it + 2 * j - 1) % slots;
-            if (lane == 0) {
-              pv(1, sp, j == 1);
-              umma_commit(empty(sp));
-            }
+          const uint64_t dk = smem_desc_sw128(s_ring + sk * kTile);
+#pragma unroll
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            const uint64_t off = (uint64_t)((ks >> 2) * (kHalfTile >> 4) + (ks & 3) * 2);
+            umma_ss(on, t_s, dq + off, dk + off, id_s, ks > 0 ? 1u : 0u);
           }
-          if (lane == 0) {
-            if (two) qk(1, sk);
-            umma_commit(empty(sk));
-            if (j + 1 == n) umma_commit(q_empty);
-          }
-          if (!wait_warp(full(sv), ((it + 2 * j + 1) / slots) & 1)) { ok = false; break; }
-          const int live = w.q.len - (w.kbeg + j) * kKT;  // keys of this tile below the end
+          umma_commit_if(on, s_full(x));
+          umma_commit_if(on, empty(sk));
+          if (j + 1 == n) umma_commit_if(on, q_empty);
+
+          if (!two && (x == 1 || both) && !(ok = pass())) break;
+          const int sv = at.slot;
+          if (!(ok = wait_warp(full(sv), at.phase))) break;
+          at.next(slots);
+          const int live = len - (run0 + (two ? j : 2 * j + x)) * kKT;
           if (live < kKT) {
-            // rows past the request's keys hold whatever the page held: as zeros
-            // they add nothing (their weights are 0, but 0 x NaN is not)
+            // Rows past the request's keys hold whatever the page held: as zeros they
+            // add nothing (their weights are 0, but 0 x NaN is not).  With two query
+            // tiles both warps write the zeros.
             const int rows = kKT - max(live, 0);
             for (int c = lane; c < rows * 8 * kHalves; c += 32) {
               const int hf = c / (rows * 8), o = c % (rows * 8);
@@ -322,211 +708,280 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
-          if (!wait_warp(p_full(0), tiles & 1)) { ok = false; break; }
+          // O (+)= P V, each half of P as soon as it is there
+          const uint64_t dv = desc_mn(s_ring + sv * kTile, kHalfTile);
+          if (!(ok = wait_warp(p_half(x), done & 1))) break;
           tc_fence_after();
-          if (lane == 0) {
-            pv(0, sv, j == 0);
-            if (!two) umma_commit(empty(sv));
-            if (j + 1 == n) umma_commit(o_full(0));
-          }
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts(on, t_o, t_s + ks * 8, dv + (uint64_t)(ks * 128), id_o,
+                    (j > 0 || ks > 0) ? 1u : 0u);
+          // all that the next step needs, so that its scores follow at once
+          turn = both;
+          other += x == 1 || both;
+          if (!two && x == 0 && both && !(ok = pass())) break;
+          if (j + 1 < n && !(ok = k_ready())) break;
+          if (!(ok = wait_warp(p_full(x), done & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks)
+            umma_ts(on, t_o, t_s + ks * 8, dv + (uint64_t)(ks * 128), id_o, 1u);
+          umma_commit_if(on, empty(sv));
+          if (j + 1 == n) umma_commit_if(on, o_full(x));
         }
         if (!ok) break;
-        if (two) {
-          if (!wait_warp(p_full(1), (tiles1++) & 1)) { ok = false; break; }
-          tc_fence_after();
-          if (lane == 0) {
-            const int sp = (it + 2 * n - 1) % slots;
-            pv(1, sp, n == 1);
-            umma_commit(empty(sp));
-            umma_commit(o_full(1));
-          }
+        if (n < n0) {  // a last step without tile 1
+          if (!(ok = pass() && take_turn() && pass())) break;
+          ++other;
         }
-        it += 2 * n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty(k));
       }
       // the products in flight end before TMEM is freed
-      if (lane == 0) umma_commit(all_done);
+      umma_commit_if(on, all_done);
       __syncwarp();
       ok &= mbar_wait(all_done, 0);
     }
   } else {
+#define LDMODE 0
+#define TURN 1
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
-    AttnWalk<kKT> w(a, pre);
-    const int x = warp >> 2;
+    const int x = warp >> 2, quarter = warp & 3;
+    const uint32_t on = elect_one();
     const int lr = tid & 127;  // row of the query tile = TMEM lane
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + kColS + x * 128 + lanes, tO = tmem + kColO + x * 128 + lanes;
-    const float c = a.scale_log2;
-    int tiles = 0, seg = 0;
-    int checked = -1;
-    bool mapped = false;
-    // Query tile 1 sits out the segments that do not need it: its barriers then
-    // do not complete a phase, and its own counts of tiles and segments go with them.
-    for (; !w.done() && ok; w.next()) {
-      if (w.r != checked) {
-        checked = w.r;
-        mapped = pages_mapped(a, w.r, w.q, lane);
-        if (!mapped && lane == 0) set_error(a.err, DFLASH_DEV_PAGE);
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + kColS + x * 128 + lanes, tO = tmem + kColO + lanes;
+    int tiles = 0;   // of tile x so far
+    int seg1 = 0;    // segments with a tile 1 so far
+    int n_rows = 0;  // meetings so far
+    // bounded, as every wait: a warp that gave up does not come
+    auto meet_rows = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(met_rows(quarter));
+      return wait_warp(met_rows(quarter), (n_rows++) & 1);
+    };
+    for (int k = 0; ok; ++k) {
+      if (!wait_warp(seg_full(k), phase(k))) { ok = false; break; }
+      const Seg& g = fx.seg[k % kSegs];
+      if (!g.more) break;
+      const bool two = g.two;
+      const int qtok = g.tok0 + (two ? x * a.ipq : 0);  // first token of the query tile
+      const int mine = min(g.tokens - (qtok - g.tok0), a.ipq), rows = mine * a.G;
+      const bool valid = lr < rows, live = quarter * 32 < rows;
+      const int n = g.steps(x), run0 = g.run(x, 0) * kKT, hop = two ? kKT : 2 * kKT;
+      const AttnReq q = {0, 0, 0, g.len};
+      int lo, hi;  // the keys that the row sees
+      {
+        const int p = g.st + qtok + a.by_g.div(min(lr, rows - 1));
+        lo = row_lo(a, p);
+        hi = row_hi(a, q, p);
       }
-      const int tok0 = w.t * a.ipt;
-      const bool whole = w.whole();
-      if (tid == 0 && !whole && w.kbeg == w.k0) {
-        const int last = w.cta_last();
-        JoinItem d;
-        d.valid = mapped;
-        d.row0 = w.q.row0;
-        d.tok0 = tok0;
-        d.tokens = w.tokens();
-        d.h = w.h;
-        d.last = last;
-        d.late = w.first ? 0 : 1;
-        d.pad = 0;
-        join[blockIdx.x] = d;
-      }
-      const int mine = w.tokens() - x * ipq;  // tokens of this query tile
-      if (mine <= 0) continue;
-      const int rows = min(mine, ipq) * a.G;
-      const int tk = tok0 + x * ipq + min(lr, rows - 1) / a.G, hg = min(lr, rows - 1) % a.G;
-      const bool valid = lr < rows;
-      const int p = w.q.st + tk;
-      const int lo = row_lo(a, p), hi = row_hi(a, w.q, p);
       // every row of the query tile sees the keys [all_lo, all_hi)
-      const int all_hi = row_hi(a, w.q, w.q.st + tok0 + x * ipq);
-      const int all_lo = row_lo(a, w.q.st + tok0 + x * ipq + min(mine, ipq) - 1);
-      float m = -INFINITY, l = 0.f;  // reference maximum (log2 units), sum
-      for (int kt = w.kbeg; kt < w.kend; ++kt, ++tiles) {
+      const int all_hi = row_hi(a, q, g.st + qtok);
+      const int all_lo = row_lo(a, g.st + qtok + mine - 1);
+      float m = -INFINITY;      // reference maximum (log2 units)
+      uint64_t l0 = 0, l1 = 0;  // sums
+      bool blind = true;        // a row of the warp has seen nothing: weights of exactly 0
+      for (int j = 0; j < n; ++j, ++tiles) {
         if (!wait_warp(s_full(x), tiles & 1)) { ok = false; break; }
-        tc_fence_after();
-        float s[128];
-        tmem_ld64<0>(tS, s);
-        tmem_ld64<64>(tS + 64, s);
-        const int k0 = kt * kKT;
-        if (k0 < all_lo || k0 + kKT > all_hi) {
-          const int l0 = lo - k0, h0 = hi - k0;
+        if (live) {
+          tc_fence_after();
+          float s[4][32];
+#if LDMODE == 0
+          tmem_ld(tS, reinterpret_cast<float(&)[128]>(s));
+#elif LDMODE == 1
+          tmem_ld_start(tS, s[0]);
+          tmem_ld_start(tS + 32, s[1]);
+          tmem_ld_start(tS + 64, s[2]);
+          tmem_ld_start(tS + 96, s[3]);
+          tmem_landed(s[0], s[1], s[2], s[3]);
+#else
+          tmem_ld(tS, reinterpret_cast<float(&)[64]>(s[0]));
+          tmem_ld(tS + 64, reinterpret_cast<float(&)[64]>(s[2]));
+#endif
+#if TURN == 0
+          mbar_arrive_if(on, s_read(x));
+#endif
+          const int k0 = run0 + j * hop;
+          if (k0 < all_lo || k0 + kKT > all_hi) {
+            const int b0 = lo - k0, b1 = hi - k0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < l0 || i >= h0) s[i] = -INFINITY;
-        }
-        float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+            for (int i = 0; i < 128; ++i)
+              if (i < b0 || i >= b1) s[i / 32][i % 32] = -INFINITY;
+          }
+          float mx[4];
 #pragma unroll
-        for (int i = 4; i < 128; i += 4) {
-          mx0 = fmaxf(mx0, s[i]);
-          mx1 = fmaxf(mx1, s[i + 1]);
-          mx2 = fmaxf(mx2, s[i + 2]);
-          mx3 = fmaxf(mx3, s[i + 3]);
-        }
-        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c;
-        if (__any_sync(0xffffffffu, valid && mx > m + kLazy)) {
-          const float mn = fmaxf(m, mx);
-          const float f = mn == -INFINITY ? 1.f : ex2_ftz(m - mn);
-          m = mn;
-          l *= f;
-          // S of this tile was issued behind the product of the tile before, so O
-          // is complete
-          if (kt > w.kbeg) {
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = s[c][0];
+#pragma unroll
+            for (int i = 1; i < 31; i += 2) mx[c] = max3(mx[c], s[c][i], s[c][i + 1]);
+            mx[c] = max3(mx[c], mx[c], s[c][31]);
+          }
+#if TURN == 1
+          mbar_arrive_if(on, s_read(x));
+#endif
+          const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2;
+          // NaN takes the branch too
+          if (__any_sync(0xffffffffu, valid && !(mt <= m + kLazy)) || blind) {
+            float mn = max3(m, m, mt);
+            // an infinite score makes the row NaN, which the polynomial would lose
+            if (mn == INFINITY) mn = NAN;
+            const float f = mn == -INFINITY ? 1.f : ex2_ftz(m - mn);
+            m = mn;
+            l0 = mul2(l0, pair(f, f));
+            l1 = mul2(l1, pair(f, f));
+            // S of this tile was issued behind the product of the tile before, so O
+            // is complete
+            if (j > 0) {
 #pragma unroll 1
-            for (int cc = 0; cc < HD; cc += 32) {
-              float o[32];
-              uint32_t u[32];
-              tmem_ld32f(tO + cc, o);
+              for (int cc = 0; cc < HD; cc += 16) {
+                float o[16];
+                uint32_t u[16];
+                tmem_ld(tO + x * 128 + cc, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-              tmem_st32(tO + cc, u);
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f);
+                tmem_st(tO + x * 128 + cc, u);
+              }
             }
+            blind = __any_sync(0xffffffffu, valid && m == -INFINITY);
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          const uint64_t c2 = pair(a.scale_log2, a.scale_log2), r2 = pair(-ref, -ref);
+          if (blind)
+            tile_weights<T, false>(s, c2, r2, tS, on, p_half(x), p_full(x), l0, l1);
+          else
+            tile_weights<T, true>(s, c2, r2, tS, on, p_half(x), p_full(x), l0, l1);
+        } else {
+          // no row of this warp is in use: its part of P is never read
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(s_read(x));
+            mbar_arrive(p_half(x));
+            mbar_arrive(p_full(x));
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t u[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float e0 = ex2_ftz(fmaf(s[hf * 64 + 2 * i], c, -ref));
-            const float e1 = ex2_ftz(fmaf(s[hf * 64 + 2 * i + 1], c, -ref));
-            l0 += e0;
-            l1 += e1;
-            // rounded to the operand type: relative error at most half a step per weight
-            u[i] = pack2<T>(e0, e1);
-          }
-          tmem_st32(tS + hf * 32, u);
-        }
-        l += l0 + l1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(x));
       }
       if (!ok) break;
 
       // ---------------------------------------------------------- end of a segment
-      if (!wait_warp(o_full(x), seg & 1)) { ok = false; break; }
-      ++seg;
+      // Where both tiles hold the same row over different keys, its two threads
+      // exchange maximum and sum, and each finishes half of the columns.
+      const bool has1 = g.steps(1) > 0, whole = g.whole;
+      const int nc = two ? HD : HD / 2, c0 = two ? 0 : x * nc;
+      if (!wait_warp(seg_info(k), phase(k))) { ok = false; break; }
+      const bool mapped = g.mapped;
+      // With two query tiles the tiles run independently, and a thread waits for its
+      // own accumulator only.  Otherwise the meeting makes sure that the other tile
+      // has come to the end of this segment, neither less nor more, before its
+      // accumulator is waited for.
+      if (n > 0 && !wait_warp(o_full(x), (x ? seg1 : k) & 1)) { ok = false; break; }
+      float l, f0 = 1.f, f1 = 0.f;  // the row's sum; weights of tile 0 (x when two) and tile 1
+      {
+        float e0, e1;
+        unpair(add2(l0, l1), e0, e1);
+        l = e0 + e1;
+      }
+      if (!two) {
+        fx.row[x][lr] = make_float2(m, l);
+        if (!meet_rows()) { ok = false; break; }
+        if (x == 1 && !wait_warp(o_full(0), k & 1)) { ok = false; break; }
+        if (x == 0 && has1 && !wait_warp(o_full(1), seg1 & 1)) { ok = false; break; }
+        const float2 r0 = fx.row[0][lr], r1 = fx.row[1][lr];
+        m = max3(r0.x, r0.x, r1.x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f0 = ex2_ftz(r0.x - ref);
+        f1 = ex2_ftz(r1.x - ref);
+        l = r0.y * f0 + r1.y * f1;
+      }
+      seg1 += has1;
       tc_fence_after();
-      T* outp = static_cast<T*>(a.out) + (int64_t)(w.q.row0 + tk) * a.out_stride +
-                (int64_t)(w.h * a.G + hg) * HD;
-      const size_t pr = (size_t)w.slot() * a.tile_rows + x * kQT + lr;
+      // the row's token and head among those of the kv head
+      const int ti = a.by_g.div(min(lr, rows - 1)), tk = qtok + ti;
+      const int hd = g.h * a.G + min(lr, rows - 1) - ti * a.G;
+      const int64_t orow = g.row0 + tk;
+      T* outp = static_cast<T*>(a.out) + orow * a.out_stride + (int64_t)hd * HD;
+      const size_t pr = (size_t)g.slot * a.tile_rows + (two ? x * kQT : 0) + lr;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      bool fin = true;
+      const bool put = valid && mapped;
+      float odd4[4] = {0.f, 0.f, 0.f, 0.f};  // not 0 once a value is not finite
+      if (live) {
 #pragma unroll 1
-      for (int cc = 0; cc < HD; cc += 32) {
-        float o[32];
-        tmem_ld32f(tO + cc, o);
+        for (int cc = c0; cc < c0 + nc; cc += 32) {
+          float o[32];
+          tmem_ld(tO + (two ? x * 128 : 0) + cc, o);
+          if (!two) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) fin &= isfinite(o[i]);
-        if (!valid) continue;
-        if (whole) {
-          if (mapped) {
-            uint4* dst = reinterpret_cast<uint4*>(outp + cc);
+            for (int i = 0; i < 32; ++i) o[i] *= f0;
+            if (has1) {
+              float o1[32];
+              tmem_ld(tO + 128 + cc, o1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                  pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                  pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], f1, o[i]);
+            }
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + pr * HD + cc);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 32; ++i) odd4[i & 3] = fmaf(o[i], 0.f, odd4[i & 3]);
+          if (!put) continue;
+          if (whole) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
+            store32(outp + cc, u, a.wide_out);
+            store32(outp + cc + 16, u + 8, a.wide_out);
+          } else {
+            uint32_t u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store32(a.part_o + pr * HD + cc + 8 * i, u + 8 * i, true);
+          }
         }
       }
       tc_fence_before();
-      if (valid && !whole)
-        *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m, l);
-      if (valid && whole && mapped && a.lse)
-        a.lse[(int64_t)(w.q.row0 + tk) * a.nq + w.h * a.G + hg] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      unsigned odd = __ballot_sync(0xffffffffu, !fin && valid && !isnan(l));
-      __syncwarp();
-      for (; odd && mapped; odd &= odd - 1) {
+      if (put && c0 == 0) {
+        if (!whole)
+          *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m, l);
+        else if (a.lse)
+          a.lse[orow * a.nq + hd] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+      const bool fin = odd4[0] + odd4[1] + (odd4[2] + odd4[3]) == 0.f;
+      unsigned odd = __ballot_sync(0xffffffffu, !fin && put && !isnan(l));
+      for (; odd; odd &= odd - 1) {
         const int src = __ffs(odd) - 1;
         const float mr = __shfl_sync(0xffffffffu, m, src), lr2 = __shfl_sync(0xffffffffu, l, src);
-        const int tk2 = __shfl_sync(0xffffffffu, tk, src), hg2 = __shfl_sync(0xffffffffu, hg, src);
+        const int tk2 = __shfl_sync(0xffffffffu, tk, src), hd2 = __shfl_sync(0xffffffffu, hd, src);
         float acc[HD / 32];
-        if (!masked_key_fallback<T, HD, kKT>(a, w.r, w.h, w.q, w.kbeg, w.kend, tk2, hg2,
-                                             mr == -INFINITY ? 0.f : mr, lane, acc))
+        AttnReq rq;
+        attn_req(a, g.r, rq);
+        if (!masked_key_fallback<T, HD>(a, g.r, g.h, rq, g.run0 * kKT, (g.run0 + g.runs) * kKT,
+                                        tk2, hd2 - g.h * a.G, mr == -INFINITY ? 0.f : mr, lane,
+                                        acc))
           continue;
-        T* o2 = static_cast<T*>(a.out) + (int64_t)(w.q.row0 + tk2) * a.out_stride +
-                (int64_t)(w.h * a.G + hg2) * HD;
-        const size_t pr2 = (size_t)w.slot() * a.tile_rows + x * kQT + (warp & 3) * 32 + src;
+        T* o2 = static_cast<T*>(a.out) + (int64_t)(g.row0 + tk2) * a.out_stride +
+                (int64_t)hd2 * HD;
+        const size_t pr2 = pr - lane + src;
 #pragma unroll
         for (int d = 0; d < HD / 32; ++d) {
           const int col = lane * (HD / 32) + d;
+          if (col < c0 || col >= c0 + nc) continue;  // the row's other thread does those
           if (whole)
             o2[col] = from_f<T>(lr2 == 0.f ? 0.f : acc[d] / lr2);
           else
             a.part_o[pr2 * HD + col] = acc[d];
         }
       }
+      // both threads of a row have read maximum, sum and accumulators
+      if (!two && !meet_rows()) { ok = false; break; }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_empty(k));
     }
   }
-  if (!ok && lane == 0) set_error(a.err, DFLASH_DEV_TIMEOUT);
+  if (!ok && lane == 0) set_error(a.err, placed ? DFLASH_DEV_TIMEOUT : DFLASH_DEV_CHECK);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // Joins the partials of the items that several CTAs shared: block (c, y) does
@@ -539,7 +994,7 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   const JoinItem d = join[blockIdx.x];
   if (!d.valid) return;
-  const int ipq = a.ipt / 2;
+  const int ipq = a.ipq;
   const int row = blockIdx.y * 32 + (threadIdx.x >> 3), x = row / kQT, lr = row % kQT;
   const int mine = min(d.tokens - x * ipq, ipq);
   if (lr >= mine * a.G) return;
@@ -587,8 +1042,8 @@ __global__ void __launch_bounds__(256)
 template <typename T, int HD>
 int launch_umma(const PagedAttnArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                 const CUtensorMap& tv, int box, void* join, cudaStream_t s) {
-  constexpr int kLimit = 227 * 1024 - 1024;  // dynamic, beside the barriers
-  const int fixed = 1024 + 2 * tile_bytes<HD>() + a.batch * 8;
+  constexpr int kLimit = 227 * 1024;
+  const int fixed = 2 * tile_bytes<HD>() + (int)sizeof(Fixed) + a.batch * 8;
   const int slots = std::min(kMaxSlots, (kLimit - fixed) / tile_bytes<HD>());
   if (slots < 4) return DFLASH_EUNSUPPORTED;
   static SmemLimit limit;
@@ -616,7 +1071,7 @@ int launch_attn_paged_umma(const PagedAttnArgs& a, int hd, int dtype, void* join
   CUtensorMap tq, tk, tv;
   if (!encode_2d(&tk, a.k_pool, rows, hd, hd, box, dtype) ||
       !encode_2d(&tv, a.v_pool, rows, hd, hd, box, dtype) ||
-      !encode_rows3(&tq, a.q, a.n_rows, a.nq, hd, a.q_stride, a.G, a.ipt / 2, dtype))
+      !encode_rows3(&tq, a.q, a.n_rows, a.nq, hd, a.q_stride, a.G, a.ipq, dtype))
     return DFLASH_ECUDA;
   TimedScope ts(s, TC_ATTN);
   if (dtype == DFLASH_BF16)

@@ -333,7 +333,7 @@ struct PagedAttnArgs;
 int attn_paged_ctas();  // CTAs of the few-row kernel's grid
 int launch_attn_paged(const PagedAttnArgs& a, int hd, int dtype, cudaStream_t s);
 // The tcgen05 kernel for many rows (attn_paged_umma.cu): items of two 128-row
-// query tiles (a.ipt / 2 tokens each), then the join of its shared items, whose
+// query tiles (a.ipq tokens each), then the join of its shared items, whose
 // descriptions take attn_paged_join_bytes() of workspace.
 int attn_paged_umma_ctas();
 size_t attn_paged_join_bytes();
