@@ -25,7 +25,9 @@
 //
 // Bound by the tensor cores and, equally, by the exponentials: 4 x 128 x 128 x
 // HD flop and 128 x 128 exponentials a tile, 1024 cycles each at head_dim 128.
-// kPoly of 8 pairs of exponentials are therefore evaluated on the FMA pipe.
+// (Evaluating a quarter of the exponentials by a polynomial on the FMA pipe was
+// slower: 512 us against 497 for a prompt of 8192 tokens; its instructions cost
+// more issue slots than the special-function unit's time is worth.)
 #include <algorithm>
 
 #include "attn_paged.cuh"
@@ -42,7 +44,6 @@ constexpr int kThreads = 384;     // the last four warps: a warpgroup of their o
 constexpr int kMaxSlots = 12;
 constexpr int kSegs = 2;          // segments described ahead
 constexpr int kBars = 2 * kMaxSlots + 8 + 3 * kSegs + 3 + 4 + 2;
-constexpr int kPoly = 2;          // of 8 pairs of exponentials, those on the FMA pipe
 constexpr float kLazy = 8.f;      // log2 growth of a row's maximum before O is rescaled
 // registers per thread: 168 at launch; 2 x 216 + 72 = 3 x 168
 constexpr int kRegSoftmax = 216, kRegOther = 72;
@@ -173,18 +174,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[32]) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : R16(v, 0), R16(v, 16), R16(v, 32), R16(v, 48)
-      : "r"(addr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[128]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
@@ -201,40 +190,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[128]) {
       : "r"(addr)
       : "memory");
 }
-// The same, there after tmem_landed.
-__device__ __forceinline__ void tmem_ld_start(uint32_t addr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : R16(v, 0), R16(v, 16)
-      : "r"(addr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       W16(v, 0)
       : "memory");
-}
-__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      W16(v, 0), W16(v, 16)
-      : "memory");
-}
-// Four pieces asked for before; the empty operands keep their uses behind the wait.
-#define L4(a, i) "+f"(a[i]), "+f"(a[i + 1]), "+f"(a[i + 2]), "+f"(a[i + 3])
-#define L16(a, i) L4(a, i), L4(a, i + 4), L4(a, i + 8), L4(a, i + 12)
-__device__ __forceinline__ void tmem_landed(float (&a)[32], float (&b)[32], float (&c)[32],
-                                            float (&d)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : L16(a, 0), L16(a, 16), L16(b, 0), L16(b, 16), L16(c, 0), L16(c, 16), L16(d, 0),
-                 L16(d, 16)
-               :
-               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -264,56 +225,25 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// The largest of three; NaN when one is NaN.
+// The largest of three that are not NaN.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-// 2^x of two values without the special-function unit: x = n + f with n the
-// nearest integer (by adding 1.5 x 2^23) and |f| <= 1/2, a degree-5 polynomial
-// for 2^f (least largest relative error, found by linear programming on a grid:
-// 2e-7 with the coefficients rounded to fp32, as good as ex2_ftz), n added to
-// its exponent.  Values below -125 give about 2^-125, which no fp32 sum next to
-// a weight of 2^-8 or more sees.  NaN does not come through.
-__device__ __forceinline__ void ex2_poly2(uint64_t x, float& r0, float& r1) {
-  float a, b;
-  unpair(x, a, b);
-  x = pair(fmaxf(a, -125.f), fmaxf(b, -125.f));
-  constexpr float kMagic = 12582912.f;
-  const uint64_t t = add2(x, pair(kMagic, kMagic));
-  const uint64_t n = add2(t, pair(-kMagic, -kMagic));
-  const uint64_t f = fma2(n, pair(-1.f, -1.f), x);
-  uint64_t p = fma2(f, pair(0.001327647129073739f, 0.001327647129073739f),
-                    pair(0.009675540961325169f, 0.009675540961325169f));
-  p = fma2(p, f, pair(0.05550713092088699f, 0.05550713092088699f));
-  p = fma2(p, f, pair(0.24022120237350464f, 0.24022120237350464f));
-  p = fma2(p, f, pair(0.6931469440460205f, 0.6931469440460205f));
-  p = fma2(p, f, pair(1.0000001192092896f, 1.0000001192092896f));
-  float p0, p1, t0, t1;
-  unpair(p, p0, p1);
-  unpair(t, t0, t1);
-  r0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  r1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
 // Keys [32 B, 32 B + 32) of a row's scores: weights 2^(c s - ref) rounded to the
 // operand type into u, their unrounded sum into l0 + l1 (pairs).
-template <typename T, bool kFast>
+template <typename T>
 __device__ __forceinline__ void weights32(const float* s, uint64_t c2, uint64_t nref2,
                                           uint32_t* u, uint64_t& l0, uint64_t& l1) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const uint64_t x = fma2(pair(s[2 * i], s[2 * i + 1]), c2, nref2);
     float e0, e1;
-    if (kFast && (i * kPoly) % 8 < kPoly) {
-      ex2_poly2(x, e0, e1);
-    } else {
-      unpair(x, e0, e1);
-      e0 = ex2_ftz(e0);
-      e1 = ex2_ftz(e1);
-    }
+    unpair(x, e0, e1);
+    e0 = ex2_ftz(e0);
+    e1 = ex2_ftz(e1);
     const uint64_t e = pair(e0, e1);
     if (i & 1) l1 = add2(l1, e); else l0 = add2(l0, e);
     // rounded to the operand type: relative error at most half a step per weight
@@ -324,14 +254,14 @@ __device__ __forceinline__ void weights32(const float* s, uint64_t c2, uint64_t 
 // A row's weights, into TMEM columns tS.., and their sum; p_half is told of the
 // first 64 keys' (late enough that nothing waits for the stores), p_full of all.
 // No branch inside, so that the instructions of all 128 keys can overlap.
-template <typename T, bool kFast>
-__device__ __forceinline__ void tile_weights(const float (&s)[4][32], uint64_t c2, uint64_t nref2,
+template <typename T>
+__device__ __forceinline__ void tile_weights(const float (&s)[128], uint64_t c2, uint64_t nref2,
                                              uint32_t tS, uint32_t on, uint32_t p_half,
                                              uint32_t p_full, uint64_t& l0, uint64_t& l1) {
   uint32_t u[4][16];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    weights32<T, kFast>(s[c], c2, nref2, u[c], l0, l1);
+    weights32<T>(s + 32 * c, c2, nref2, u[c], l0, l1);
     if (c < 2) tmem_st(tS + c * 16, u[c]);
     if (c == 2) {
       tmem_wait_st();
@@ -650,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       // The tiles take turns: a tile's next scores start when the other one's threads
-      // have their maxima, so that one is in its exponentials while the products of
+      // have read theirs, so that one is in its exponentials while the products of
       // the other run.  Left alone they fall into step, and wait for the
       // special-function unit and for the products together.  Tile 1 waits in every
       // step of tile 0, tile 0 after every step of tile 1, so that neither passes
@@ -743,8 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok &= mbar_wait(all_done, 0);
     }
   } else {
-#define LDMODE 0
-#define TURN 1
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
     const int x = warp >> 2, quarter = warp & 3;
@@ -782,51 +710,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_lo = row_lo(a, g.st + qtok + mine - 1);
       float m = -INFINITY;      // reference maximum (log2 units)
       uint64_t l0 = 0, l1 = 0;  // sums
-      bool blind = true;        // a row of the warp has seen nothing: weights of exactly 0
       for (int j = 0; j < n; ++j, ++tiles) {
         if (!wait_warp(s_full(x), tiles & 1)) { ok = false; break; }
         if (live) {
           tc_fence_after();
-          float s[4][32];
-#if LDMODE == 0
-          tmem_ld(tS, reinterpret_cast<float(&)[128]>(s));
-#elif LDMODE == 1
-          tmem_ld_start(tS, s[0]);
-          tmem_ld_start(tS + 32, s[1]);
-          tmem_ld_start(tS + 64, s[2]);
-          tmem_ld_start(tS + 96, s[3]);
-          tmem_landed(s[0], s[1], s[2], s[3]);
-#else
-          tmem_ld(tS, reinterpret_cast<float(&)[64]>(s[0]));
-          tmem_ld(tS + 64, reinterpret_cast<float(&)[64]>(s[2]));
-#endif
-#if TURN == 0
+          float s[128];
+          tmem_ld(tS, s);
           mbar_arrive_if(on, s_read(x));
-#endif
           const int k0 = run0 + j * hop;
           if (k0 < all_lo || k0 + kKT > all_hi) {
             const int b0 = lo - k0, b1 = hi - k0;
 #pragma unroll
             for (int i = 0; i < 128; ++i)
-              if (i < b0 || i >= b1) s[i / 32][i % 32] = -INFINITY;
+              if (i < b0 || i >= b1) s[i] = -INFINITY;
           }
-          float mx[4];
+          float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx[c] = s[c][0];
+          for (int i = 4; i < 124; i += 8)
 #pragma unroll
-            for (int i = 1; i < 31; i += 2) mx[c] = max3(mx[c], s[c][i], s[c][i + 1]);
-            mx[c] = max3(mx[c], mx[c], s[c][31]);
-          }
-#if TURN == 1
-          mbar_arrive_if(on, s_read(x));
-#endif
-          const float mt = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2;
-          // NaN takes the branch too
-          if (__any_sync(0xffffffffu, valid && !(mt <= m + kLazy)) || blind) {
-            float mn = max3(m, m, mt);
-            // an infinite score makes the row NaN, which the polynomial would lose
-            if (mn == INFINITY) mn = NAN;
+            for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], s[i + 2 * c], s[i + 2 * c + 1]);
+          mx[0] = max3(mx[0], s[124], s[125]);
+          mx[1] = max3(mx[1], s[126], s[127]);
+          const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+          if (__any_sync(0xffffffffu, valid && mt > m + kLazy)) {
+            const float mn = fmaxf(m, mt);
             const float f = mn == -INFINITY ? 1.f : ex2_ftz(m - mn);
             m = mn;
             l0 = mul2(l0, pair(f, f));
@@ -844,14 +751,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st(tO + x * 128 + cc, u);
               }
             }
-            blind = __any_sync(0xffffffffu, valid && m == -INFINITY);
           }
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t c2 = pair(a.scale_log2, a.scale_log2), r2 = pair(-ref, -ref);
-          if (blind)
-            tile_weights<T, false>(s, c2, r2, tS, on, p_half(x), p_full(x), l0, l1);
-          else
-            tile_weights<T, true>(s, c2, r2, tS, on, p_half(x), p_full(x), l0, l1);
+          tile_weights<T>(s, c2, r2, tS, on, p_half(x), p_full(x), l0, l1);
         } else {
           // no row of this warp is in use: its part of P is never read
           __syncwarp();
@@ -888,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x == 1 && !wait_warp(o_full(0), k & 1)) { ok = false; break; }
         if (x == 0 && has1 && !wait_warp(o_full(1), seg1 & 1)) { ok = false; break; }
         const float2 r0 = fx.row[0][lr], r1 = fx.row[1][lr];
-        m = max3(r0.x, r0.x, r1.x);
+        m = fmaxf(r0.x, r1.x);
         const float ref = m == -INFINITY ? 0.f : m;
         f0 = ex2_ftz(r0.x - ref);
         f1 = ex2_ftz(r1.x - ref);
