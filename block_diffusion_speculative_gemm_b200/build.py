@@ -19,6 +19,10 @@ LIB = os.path.join(HERE, "libdflash.so")
 # and skip the access, for test runs (the stand-in for a memory checker)
 LIB_CHECKED = os.path.join(HERE, "libdflash_checked.so")
 
+# Python calls of the target-side attention operators (csrc/binding.cpp)
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_calls.so")
+
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
@@ -81,7 +85,32 @@ def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = 
     return lib
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compiles csrc/binding.cpp against this Python's and torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "dflash.h"), __file__]
+    if not force and os.path.exists(BINDING) and all(
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    nvcc_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))),
+                                "include")
+    inc = [INCLUDE, sysconfig.get_paths()["include"], nvcc_include, *include_paths()]
+    tmp = BINDING + ".tmp"
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+          "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f"-isystem{p}" for p in inc], "-o", tmp, BINDING_SRC,
+          *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+          "-lc10"], verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
+    build_binding(force="--force" in sys.argv, verbose=True)
     build(force="--force" in sys.argv, verbose=True,
           extra=("-Xptxas", "-v") if "--ptxas-v" in sys.argv else (),
           checked="--checked" in sys.argv)

@@ -608,69 +608,30 @@ def verify_sampled(target_logits: torch.Tensor, draft_logits: torch.Tensor,
 
 
 # ---- attention of the target model over paged K/V ------------------------
-_ATTN_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_calls = None
 
 
-def _need_here(dev: int, **tensors):
-    """Every tensor given is on the current CUDA device."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device {dev}, is on {t.device}")
-
-
-def _rows3(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
-    """Checks a [n_rows, heads, head_dim] operand with contiguous heads (a view into a fused
-    projection, say) and returns its row stride in elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [n_rows, heads, head_dim]")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, hd = t.shape
-    if shape is not None and (n, h, hd) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and hd > 1) or (s1 != hd and h > 1):
-        raise ValueError(f"{name}'s heads must be contiguous")
-    return s0 if n > 1 else max(s0, h * hd)
-
-
-def _need_gain(g, name, t):
-    if g is None:
-        return None
-    _need(g, name, t.dtype, (t.shape[2],))
-    return g.data_ptr()
-
-
-def _need_rope(rope, hd):
-    if rope is None:
-        return None, 0
-    _need(rope, "rope", torch.float32)
-    if rope.dim() != 3 or rope.shape[0] != 2 or rope.shape[2] * 2 != hd:
-        raise ValueError("rope must be [2, max_pos, head_dim / 2]")
-    return rope.data_ptr(), rope.shape[1]
-
-
-def _need_pool(k_pool, v_pool, page_table, n_kv, hd, batch):
-    _need(k_pool, "k_pool")
-    _need(v_pool, "v_pool", k_pool.dtype, k_pool.shape)
-    if k_pool.dtype not in _ATTN_DT:
-        raise TypeError(f"k_pool: no cache of {k_pool.dtype}")
-    if k_pool.dim() != 4 or k_pool.shape[1] != n_kv or k_pool.shape[3] != hd:
-        raise ValueError("k_pool must be [n_pages, n_kv, page_size, head_dim]")
-    _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != batch:
-        raise ValueError("page_table must be [batch, max_pages]")
-    return k_pool.shape[0], k_pool.shape[2], page_table.shape[1]
+def calls():
+    """The module of these operators' calls (csrc/binding.cpp), bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise RuntimeError("_calls.so is missing or does not load: build it with "
+                               "`python -m block_diffusion_speculative_gemm_b200.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib().dflash_qk_norm_rope, lib().dflash_kv_append_paged,
+            lib().dflash_attention_paged)))
+        _calls = m
+    return _calls
 
 
 def rope_table(max_pos: int, head_dim: int, base: float, device=None, stream=None) -> torch.Tensor:
     """Rotation table [2, max_pos, head_dim / 2] (cosines, sines) of angle p * base^(-2i/head_dim)."""
     t = torch.empty((2, max_pos, head_dim // 2), dtype=torch.float32, device=device or "cuda")
-    _need_here(torch.cuda.current_device(), table=t)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the table must be on the current CUDA device, is on {t.device}")
     _check("dflash_rope_table", lib().dflash_rope_table(t.data_ptr(), max_pos, head_dim,
                                                         float(base), _stream(stream)))
     return t
@@ -697,33 +658,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], g_q: Opti
     """RMSNorm of every query and key head (``g_q`` / ``g_k`` given) and the rotate-half
     rotation (``rope`` given) in one pass; ``q`` or ``k`` may be None.  See
     dflash_qk_norm_rope in include/dflash.h."""
-    t = q if q is not None else k
-    if t is None:
-        raise ValueError("q and k are both None")
-    qs = qo = ks = ko = nq = nkv = 0
-    if q is not None:
-        qs, nq = _rows3(q, "q"), q.shape[1]
-        qo = _rows3(q_out, "q_out", q.dtype, tuple(q.shape))
-    if k is not None:
-        ks, nkv = _rows3(k, "k", t.dtype, (t.shape[0], k.shape[1], t.shape[2])), k.shape[1]
-        ko = _rows3(k_out, "k_out", k.dtype, tuple(k.shape))
-    if t.dtype not in _ATTN_DT:
-        raise TypeError(f"q: unsupported type {t.dtype}")
-    n, hd = t.shape[0], t.shape[2]
-    batch = start_pos.numel()
-    gq, gk = _need_gain(g_q, "g_q", t), _need_gain(g_k, "g_k", t)
-    rp, max_pos = _need_rope(rope, hd)
-    _need(cu_rows, "cu_rows", torch.int32, (batch + 1,))
-    _need(start_pos, "start_pos", torch.int32, (batch,))
-    _need(ws, "ws", torch.uint8)
-    _need_here(torch.cuda.current_device(), q=q, k=k, g_q=g_q, g_k=g_k, rope=rope, cu_rows=cu_rows,
-               start_pos=start_pos, q_out=q_out if q is not None else None,
-               k_out=k_out if k is not None else None, ws=ws)
-    st = lib().dflash_qk_norm_rope(
-        q.data_ptr() if nq else None, qs, k.data_ptr() if nkv else None, ks, _ATTN_DT[t.dtype], gq,
-        gk, eps, rp, max_pos, cu_rows.data_ptr(), start_pos.data_ptr(), batch, n, nq, nkv, hd,
-        q_out.data_ptr() if nq else None, qo, k_out.data_ptr() if nkv else None, ko, ws.data_ptr(),
-        ws.numel(), _stream(stream))
+    st = (_calls or calls()).qk_norm_rope(q, k, g_q, g_k, rope, cu_rows, start_pos, q_out, k_out,
+                                          ws, eps, stream)
     if st:
         _check("dflash_qk_norm_rope", st)
 
@@ -735,25 +671,8 @@ def kv_append_paged(k: torch.Tensor, v: torch.Tensor, g_k: Optional[torch.Tensor
     """Writes a chunk's keys (normalised with ``g_k``, rotated with ``rope``) and values into the
     pages of one layer's pools [n_pages, n_kv, page_size, head_dim].  See
     dflash_kv_append_paged in include/dflash.h."""
-    ks = _rows3(k, "k")
-    vs = _rows3(v, "v", k.dtype, tuple(k.shape))
-    if k.dtype not in _ATTN_DT:
-        raise TypeError(f"k: unsupported type {k.dtype}")
-    n, nkv, hd = k.shape
-    batch = start_pos.numel()
-    gk = _need_gain(g_k, "g_k", k)
-    rp, max_pos = _need_rope(rope, hd)
-    _need(cu_rows, "cu_rows", torch.int32, (batch + 1,))
-    _need(start_pos, "start_pos", torch.int32, (batch,))
-    n_pages, page, max_pages = _need_pool(k_pool, v_pool, page_table, nkv, hd, batch)
-    _need(ws, "ws", torch.uint8)
-    _need_here(torch.cuda.current_device(), k=k, v=v, g_k=g_k, rope=rope, cu_rows=cu_rows,
-               start_pos=start_pos, k_pool=k_pool, v_pool=v_pool, page_table=page_table, ws=ws)
-    st = lib().dflash_kv_append_paged(
-        k.data_ptr(), ks, v.data_ptr(), vs, _ATTN_DT[k.dtype], gk, eps, rp, max_pos,
-        cu_rows.data_ptr(), start_pos.data_ptr(), batch, n, nkv, hd, k_pool.data_ptr(),
-        v_pool.data_ptr(), _ATTN_DT[k_pool.dtype], n_pages, page, page_table.data_ptr(), max_pages,
-        ws.data_ptr(), ws.numel(), _stream(stream))
+    st = (_calls or calls()).kv_append_paged(k, v, g_k, rope, cu_rows, start_pos, k_pool, v_pool,
+                                             page_table, ws, eps, stream)
     if st:
         _check("dflash_kv_append_paged", st)
 
@@ -766,32 +685,9 @@ def attention_paged(q: torch.Tensor, cu_rows: torch.Tensor, start_pos: torch.Ten
     """Attention of each request's rows over its paged keys; ``scale`` defaults to
     head_dim^-0.5, ``lse`` (fp32 [n_rows, n_q]) receives the log-sum-exp of every row.  See
     dflash_attention_paged in include/dflash.h."""
-    qs = _rows3(q, "q")
-    os_ = _rows3(out, "out", q.dtype, tuple(q.shape))
-    if q.dtype not in _ATTN_DT:
-        raise TypeError(f"q: unsupported type {q.dtype}")
-    n, nq, hd = q.shape
-    batch = start_pos.numel()
-    _need(cu_rows, "cu_rows", torch.int32, (batch + 1,))
-    _need(start_pos, "start_pos", torch.int32, (batch,))
-    if kv_len is not None:
-        _need(kv_len, "kv_len", torch.int32, (batch,))
-    if k_pool.dtype != q.dtype:
-        raise TypeError(f"k_pool must be {q.dtype}, got {k_pool.dtype}")
-    nkv = k_pool.shape[1] if k_pool.dim() == 4 else 0
-    n_pages, page, max_pages = _need_pool(k_pool, v_pool, page_table, nkv, hd, batch)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (n, nq))
-    _need(ws, "ws", torch.uint8)
-    _need_here(torch.cuda.current_device(), q=q, cu_rows=cu_rows, start_pos=start_pos,
-               kv_len=kv_len, k_pool=k_pool, v_pool=v_pool, page_table=page_table, out=out,
-               lse=lse, ws=ws)
-    st = lib().dflash_attention_paged(
-        q.data_ptr(), qs, _ATTN_DT[q.dtype], cu_rows.data_ptr(), start_pos.data_ptr(),
-        None if kv_len is None else kv_len.data_ptr(), batch, n, nq, nkv, hd, k_pool.data_ptr(),
-        v_pool.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
-        hd ** -0.5 if scale is None else scale, bool(causal), window, out.data_ptr(), os_,
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    st = (_calls or calls()).attention_paged(q, cu_rows, start_pos, kv_len, k_pool, v_pool,
+                                             page_table, out, ws, scale, causal, window, lse,
+                                             stream)
     if st:
         _check("dflash_attention_paged", st)
 
