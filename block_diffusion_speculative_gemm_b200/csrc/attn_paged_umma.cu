@@ -304,20 +304,6 @@ struct Fixed {
 };
 static_assert(sizeof(Fixed) % 8 == 0, "the units follow");
 
-// Test of an mbarrier's phase that sleeps up to kNapNs until it completes.
-constexpr uint32_t kNapNs = 20000;
-__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kNapNs)
-      : "memory");
-  return ok != 0;
-}
-
 // A position of the ring, by counting: a division by the number of slots would
 // take longer than a product's instructions.
 struct RingPos {
@@ -406,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // that finds the phase incomplete sleeps for a while, so that waiting warps
   // leave the issue slots to the others
   auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-    if (try_wait_for(b, parity)) return true;
+    if (mbar_try_wait_nap(b, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!try_wait_for(b, parity)) {
+    while (!mbar_try_wait_nap(b, parity)) {
       if (*(volatile int*)&fx.abort || global_ns() - t0 > kWaitNs) {
         *(volatile int*)&fx.abort = 1;
         return false;

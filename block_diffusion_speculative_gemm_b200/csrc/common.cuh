@@ -156,6 +156,29 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
+// Test of an mbarrier's phase that sleeps up to kNapNs until it completes.
+constexpr uint32_t kNapNs = 20000;
+__device__ __forceinline__ bool mbar_try_wait_nap(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kNapNs)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait by such tests, which leave the issue slots to other warps.
+__device__ __forceinline__ bool mbar_wait_nap(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait_nap(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait_nap(bar, parity))
+    if (global_ns() - t0 > kWaitNs) return false;
+  return true;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
