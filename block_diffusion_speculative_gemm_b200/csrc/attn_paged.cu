@@ -1,19 +1,19 @@
-// Paged chunk attention for few rows per kv head (single tokens, drafted
-// blocks): softmax(scale Q K^T) V over a paged cache in one pass, on
+// Paged chunk attention for at most 16 rows per kv head and request (single
+// tokens, mostly): softmax(scale Q K^T) V over a paged cache in one pass, on
 // mma.sync m16n8k16 with fp32 accumulators.
 //
 //   S = Q K^T;  m' = max(m, max S);  P = 2^(S c - m' c), c = scale log2(e);
 //   l' = l 2^((m - m') c) + sum P;   O' = O 2^((m - m') c) + P V
 //
-// A CTA is one producer warp, which streams 64-key K and V tiles into a ring
-// of shared-memory slots with TMA (one box per page piece), and four compute
-// warps.  16 WM rows of an item go to WM warps; the 4 / WM warps that share
-// rows split the keys of every tile and are joined at the end of a segment.
-// The softmax state and O stay in registers, Q too, P goes from the S
-// accumulators to the next product's operand without leaving the thread.
-// Bound by memory: the keys and values of an item are read once for all its
-// rows, 4 rows flop per byte.  The producer runs on over segment boundaries,
-// so the ring stays full while a segment is finished.
+// A CTA is one producer warp, which finds the CTA's segments, describes them to
+// the others, and streams 64-key K and V tiles into a ring of shared-memory slots
+// with TMA (one box per page piece), and four compute warps, which split the keys
+// of every tile and are joined at the end of a segment.  The softmax state and O
+// stay in registers, Q too, P goes from the S accumulators to the next product's
+// operand without leaving the thread.  Bound by memory: the keys and values of an
+// item are read once for all its rows, 4 rows flop per byte.  The producer runs on
+// over segment boundaries, so the ring stays full while a segment is finished, and
+// two CTAs share an SM.
 //
 // Every CTA has the same number of key tiles (attn_paged.cuh); an item shared
 // by several CTAs is left as partials (O, max, sum), and the CTA that counts
@@ -33,7 +33,17 @@ constexpr int kSlots = 6;                 // ring slots, each a K or a V tile
 constexpr int kPassCols = 64;             // O columns joined at a time
 
 template <int HD> constexpr int slot_bytes() { return kKT * HD * 2; }
-template <int WM> constexpr int scratch_bytes() { return (4 / WM - 1) * WM * 16 * kPassCols * 4; }
+constexpr int kScratch = 3 * 16 * kPassCols * 4;
+constexpr int kSegs = 4;                  // segments described ahead
+
+// A segment of the CTA's work, as the producer describes it.
+struct Seg {
+  int more;               // 0: the end
+  int r, h, row0, st, n, len;
+  int tok0, tokens;
+  int kbeg, kend, whole;
+  int slot, c0, c1, late;  // partial slot; CTAs that share the item, its place in c0
+};
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -83,13 +93,13 @@ __device__ __forceinline__ bool bar_compute_or(bool v) {
   return r != 0;
 }
 
-template <typename T, int HD, int WM>
+template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ PagedAttnArgs a, int box) {
   pdl_trigger();
-  constexpr int NK = 4 / WM;          // key groups
+  constexpr int NK = 4;               // key groups, one a warp
   constexpr int KW = kKT / NK;        // keys of a tile per warp
   constexpr int kNT = KW / 8;         // S column blocks
   constexpr int kSlot = slot_bytes<HD>();
@@ -98,8 +108,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   float* scratch = reinterpret_cast<float*>(smem + kSlots * kSlot);
-  long long* pre = reinterpret_cast<long long*>(smem + kSlots * kSlot + scratch_bytes<WM>());
-  __shared__ __align__(8) uint64_t bars[2 * kSlots];
+  long long* pre = reinterpret_cast<long long*>(smem + kSlots * kSlot + kScratch);
+  __shared__ __align__(8) uint64_t bars[2 * kSlots + 2 * kSegs];
+  __shared__ Seg segs[kSegs];
   __shared__ float s_ml[4][16][2];
   __shared__ int s_abort, s_last;
 
@@ -107,22 +118,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t s_base = smem_u32(smem);
   auto full = [&](int s) { return smem_u32(&bars[s]); };
   auto empty = [&](int s) { return smem_u32(&bars[kSlots + s]); };
+  auto seg_full = [&](int k) { return smem_u32(&bars[2 * kSlots + k % kSegs]); };
+  auto seg_empty = [&](int k) { return smem_u32(&bars[2 * kSlots + kSegs + k % kSegs]); };
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 4);
     }
+    for (int k = 0; k < kSegs; ++k) {
+      mbar_init(seg_full(k), 1);
+      mbar_init(seg_empty(k), 4);
+    }
     fence_barrier_init();
     s_abort = 0;
   }
+  if (tid < 2) tma_prefetch_desc(tid == 0 ? &tmK : &tmV);
+  __syncthreads();
   pdl_wait();
-  attn_plan<HD, kKL>(a, pre);  // ends with a barrier
+  if (a.batch > 32) attn_plan<HD, kKL>(a, pre);  // ends with a barrier
 
   // a bounded wait that also gives up once another warp has given up
   auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-    if (mbar_try_wait(b, parity)) return true;
+    if (mbar_try_wait_nap(b, parity)) return true;
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(b, parity)) {
+    while (!mbar_try_wait_nap(b, parity)) {
       if (*(volatile int*)&s_abort || global_ns() - t0 > kWaitNs) {
         *(volatile int*)&s_abort = 1;
         return false;
@@ -131,7 +150,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     return true;
   };
   bool ok = true;
-  AttnWalk<kKL> w(a, pre);
   const int rows_all = a.n_pages * a.nkv * a.page;  // a row past the pools: TMA fills zeros
 
   if (warp == 4) {
@@ -139,9 +157,48 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t pol = policy_evict_first();
     const int per = kKT / box;  // boxes per tile
     int it = 0;                 // ring position
-    for (; !w.done() && ok; w.next()) {
+    if (a.batch <= 32) attn_plan_warp<HD, kKL>(a, pre);
+    AttnWalk<kKL> w(a, pre);
+    for (int k = 0; ok; w.next(), ++k) {
+      if (k >= kSegs &&
+          !__all_sync(0xffffffffu, wait(seg_empty(k), (uint32_t)(k / kSegs - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      Seg& d = segs[k % kSegs];
+      if (w.done()) {
+        if (lane == 0) {
+          d.more = 0;
+          mbar_arrive(seg_full(k));
+        }
+        break;
+      }
       const int32_t* tab = a.table + (int64_t)w.r * a.max_pages;
       int ent = 0, ent_base = -1;
+      auto describe = [&]() {
+        const bool whole = w.whole();
+        const int c0 = whole ? 0 : w.cta_first(), c1 = whole ? 0 : w.cta_last();
+        if (lane == 0) {
+          d.more = 1;
+          d.r = w.r;
+          d.h = w.h;
+          d.row0 = w.q.row0;
+          d.st = w.q.st;
+          d.n = w.q.n;
+          d.len = w.q.len;
+          d.tok0 = w.t * a.ipt;
+          d.tokens = w.tokens();
+          d.kbeg = w.kbeg;
+          d.kend = w.kend;
+          d.whole = whole;
+          d.slot = w.slot();
+          d.c0 = c0;
+          d.c1 = c1;
+          d.late = whole ? 0 : w.later_in(c0);
+          mbar_arrive(seg_full(k));
+        }
+        __syncwarp();
+      };
       for (int kt = w.kbeg; kt < w.kend && ok; ++kt) {
         // the pool rows of the tile's boxes, looked up 32 boxes at a time
         const int b0 = (kt - w.kbeg) * per;
@@ -158,6 +215,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++it) {
+          // the description behind the first tile that has room (the compute warps
+          // free no slot before they have it)
+          if (kt == w.kbeg && kv == 0 && it >= kSlots) describe();
           const int s = it % kSlots;
           if (it >= kSlots) {
             ok = __all_sync(0xffffffffu, wait(empty(s), ((it / kSlots) - 1) & 1));
@@ -174,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tma_load_2d(dst + hf * kHalfTile, kv ? &tmV : &tmK, full(s), hf * 64, y, pol);
             }
           }
+          if (kt == w.kbeg && kv == 1 && it < kSlots) describe();
         }
       }
     }
@@ -181,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int j = max(0, it - kSlots); j < it; ++j) ok &= mbar_wait(full(j % kSlots), (j / kSlots) & 1);
   } else {
     // ------------------------------------------------------------ compute
-    const int wm = warp % WM, wk = warp / WM;
+    const int wk = warp;
     const int g8 = lane >> 2, t2 = (lane & 3) * 2;
     const T* qg = static_cast<const T*>(a.q);
     // ldmatrix addresses: K rows are keys (operand as stored), V transposed
@@ -189,28 +250,37 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
     int it = 0, checked = -1;
     bool mapped = false;
-    for (; !w.done() && ok; w.next()) {
+    for (int seg = 0;; ++seg) {
+      // a wait that gave up ends all compute warps together, at the next meeting
+      ok = __all_sync(0xffffffffu, wait(seg_full(seg), (uint32_t)(seg / kSegs) & 1));
+      if (bar_compute_or(!ok)) {
+        ok = false;
+        break;
+      }
+      const Seg& w = segs[seg % kSegs];
+      if (!w.more) break;
+      const AttnReq q = {w.row0, w.n, w.st, w.len};
       if (w.r != checked) {
         checked = w.r;
-        mapped = pages_mapped(a, w.r, w.q, lane);
+        mapped = pages_mapped(a, w.r, q, lane);
         if (!mapped && lane == 0) set_error(a.err, DFLASH_DEV_PAGE);
       }
-      const int tok0 = w.t * a.ipt, R = w.tokens() * a.G;
+      const int tok0 = w.tok0, R = w.tokens * a.G, kbeg = w.kbeg, kend = w.kend;
       // this thread's two rows: token, query head within the group
       int row[2], tok[2], hg[2], lo[2], hi[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        row[j] = wm * 16 + g8 + 8 * j;
+        row[j] = g8 + 8 * j;
         const int rr = min(row[j], R - 1);
         tok[j] = tok0 + a.by_g.div(rr);
         hg[j] = rr - (tok[j] - tok0) * a.G;
-        lo[j] = row_lo(a, w.q.st + tok[j]);
-        hi[j] = row_hi(a, w.q, w.q.st + tok[j]);
+        lo[j] = row_lo(a, q.st + tok[j]);
+        hi[j] = row_hi(a, q, q.st + tok[j]);
       }
       uint32_t qf[HD / 16][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const T* src = qg + (int64_t)(w.q.row0 + tok[j]) * a.q_stride +
+        const T* src = qg + (int64_t)(q.row0 + tok[j]) * a.q_stride +
                        (int64_t)(w.h * a.G + hg[j]) * HD + t2;
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
@@ -219,15 +289,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       // every row of the item sees the keys [all_lo, all_hi)
-      const int all_hi = row_hi(a, w.q, w.q.st + tok0);
-      const int all_lo = row_lo(a, w.q.st + tok0 + w.tokens() - 1);
+      const int all_hi = row_hi(a, q, q.st + tok0);
+      const int all_lo = row_lo(a, q.st + tok0 + w.tokens - 1);
       float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
-      for (int kt = w.kbeg; kt < w.kend && ok; ++kt, it += 2) {
+      for (int kt = kbeg; kt < kend && ok; ++kt, it += 2) {
         const int sk = it % kSlots, sv = (it + 1) % kSlots;
         if (!__all_sync(0xffffffffu, wait(full(sk), (it / kSlots) & 1))) { ok = false; break; }
         const int key0 = kt * kKT + wk * KW;  // this warp's first key
@@ -290,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         const uint32_t vb = s_base + sv * kSlot + (uint32_t)(wk * KW) * 128;
-        const bool tail = key0 + KW > w.q.len;
+        const bool tail = key0 + KW > q.len;
 #pragma unroll
         for (int k2 = 0; k2 < KW / 16; ++k2) {
           // P rounded to the operand type: relative error at most half a step per weight
@@ -305,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int key = key0 + k2 * 16 + j * 8 + t2;
-              keep[j] = key + 1 < w.q.len ? 0xffffffffu : key < w.q.len ? 0xffffu : 0u;
+              keep[j] = key + 1 < q.len ? 0xffffffffu : key < q.len ? 0xffffu : 0u;
             }
 #pragma unroll
           for (int d = 0; d < HD / 16; ++d) {
@@ -348,11 +418,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int j = 0; j < 2; ++j) {
           float M = -INFINITY, L = 0.f;
 #pragma unroll
-          for (int k = 0; k < NK; ++k) M = fmaxf(M, s_ml[k * WM + wm][g8 + 8 * j][0]);
+          for (int k = 0; k < NK; ++k) M = fmaxf(M, s_ml[k][g8 + 8 * j][0]);
           const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
           for (int k = 0; k < NK; ++k)
-            L += s_ml[k * WM + wm][g8 + 8 * j][1] * ex2_ftz(s_ml[k * WM + wm][g8 + 8 * j][0] - ref);
+            L += s_ml[k][g8 + 8 * j][1] * ex2_ftz(s_ml[k][g8 + 8 * j][0] - ref);
           const float f = ex2_ftz(m[j] - ref);
           m[j] = M;
           l[j] = L;
@@ -366,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int pass = 0; pass < HD / kPassCols; ++pass) {
           constexpr int kB = kPassCols / 8;
           if (wk > 0) {
-            float* dst = scratch + (size_t)((wk - 1) * WM + wm) * 16 * kPassCols;
+            float* dst = scratch + (size_t)(wk - 1) * 16 * kPassCols;
 #pragma unroll
             for (int i = 0; i < kB; ++i)
 #pragma unroll
@@ -378,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (wk == 0) {
 #pragma unroll
             for (int k = 1; k < NK; ++k) {
-              const float* src = scratch + (size_t)((k - 1) * WM + wm) * 16 * kPassCols;
+              const float* src = scratch + (size_t)(k - 1) * 16 * kPassCols;
 #pragma unroll
               for (int i = 0; i < kB; ++i)
 #pragma unroll
@@ -393,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           bar_compute();
         }
       }
-      const bool whole = w.whole();
+      const bool whole = w.whole;
       T* outp = static_cast<T*>(a.out);
       if (wk == 0) {
         unsigned odd[2];
@@ -407,18 +477,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (whole) {
             if (mapped) {
               const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
-              T* dst = outp + (int64_t)(w.q.row0 + tok[j]) * a.out_stride +
+              T* dst = outp + (int64_t)(q.row0 + tok[j]) * a.out_stride +
                        (int64_t)(w.h * a.G + hg[j]) * HD + t2;
 #pragma unroll
               for (int i = 0; i < HD / 8; ++i)
                 *reinterpret_cast<uint32_t*>(dst + i * 8) =
                     pack2<T>(o[i][2 * j] * inv, o[i][2 * j + 1] * inv);
               if (a.lse && (lane & 3) == 0)
-                a.lse[(int64_t)(w.q.row0 + tok[j]) * a.nq + w.h * a.G + hg[j]] =
+                a.lse[(int64_t)(q.row0 + tok[j]) * a.nq + w.h * a.G + hg[j]] =
                     l[j] == 0.f ? -INFINITY : (m[j] + log2f(l[j])) * 0.6931471805599453f;
             }
           } else {
-            const size_t pr = (size_t)w.slot() * a.tile_rows + row[j];
+            const size_t pr = (size_t)w.slot * a.tile_rows + row[j];
 #pragma unroll
             for (int i = 0; i < HD / 8; ++i)
               *reinterpret_cast<float2*>(a.part_o + pr * HD + i * 8 + t2) =
@@ -440,18 +510,18 @@ __global__ void __launch_bounds__(kThreads, 2)
               const int hh = __shfl_sync(0xffffffffu, hg[j], rr * 4);
               const int pr = __shfl_sync(0xffffffffu, row[j], rr * 4);
               float acc[HD / 32];
-              if (!masked_key_fallback<T, HD>(a, w.r, w.h, w.q, w.kbeg * kKT, w.kend * kKT, tk, hh,
+              if (!masked_key_fallback<T, HD>(a, w.r, w.h, q, kbeg * kKT, kend * kKT, tk, hh,
                                                    mr == -INFINITY ? 0.f : mr, lane, acc))
                 continue;
 #pragma unroll
               for (int d = 0; d < HD / 32; ++d) {
                 const int col = lane * (HD / 32) + d;
                 if (whole)
-                  outp[(int64_t)(w.q.row0 + tk) * a.out_stride +
+                  outp[(int64_t)(q.row0 + tk) * a.out_stride +
                        (int64_t)(w.h * a.G + hh) * HD + col] =
                       from_f<T>(lr == 0.f ? 0.f : acc[d] / lr);
                 else
-                  a.part_o[((size_t)w.slot() * a.tile_rows + pr) * HD + col] = acc[d];
+                  a.part_o[((size_t)w.slot * a.tile_rows + pr) * HD + col] = acc[d];
               }
             }
         }
@@ -460,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the CTA that finishes last joins the item's partials in CTA order
         __threadfence();
         bar_compute();
-        const int c0 = w.cta_first(), c1 = w.cta_last(), late = w.later_in(c0);
+        const int c0 = w.c0, c1 = w.c1, late = w.late;
         auto slot_row = [&](int x, int rr) {
           return (size_t)(2 * x + (x == c0 ? late : 0)) * a.tile_rows + rr;
         };
@@ -472,65 +542,77 @@ __global__ void __launch_bounds__(kThreads, 2)
         bar_compute();
         if (s_last && mapped) {
           __threadfence();
-          for (int idx = tid; idx < R * (HD / 4); idx += kCompute) {
-            const int rr = idx / (HD / 4), c4 = (idx % (HD / 4)) * 4;
+          // a warp a row: the lanes take the partials' maxima and sums side by side,
+          // then columns
+          for (int rr = warp; rr < R; rr += 4) {
             float M = -INFINITY;
-            for (int x = c0; x <= c1; ++x)
+            for (int x = c0 + lane; x <= c1; x += 32)
               M = fmaxf(M, __ldcg(a.part_ml + slot_row(x, rr) * 2));
+            M = warp_max(M);
             const float ref = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int x = c0; x <= c1; ++x) {
-              const size_t pr = slot_row(x, rr);
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + pr * 2));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * HD + c4));
-              const float f = ex2_ftz(ml.x - ref);
-              L += ml.y * f;
-              s.x += v.x * f;
-              s.y += v.y * f;
-              s.z += v.z * f;
-              s.w += v.w * f;
+            constexpr int V = HD / 32;
+            float L = 0.f, acc[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            for (int x0 = c0; x0 <= c1; x0 += 32) {
+              float f = 0.f, fl = 0.f;
+              if (x0 + lane <= c1) {
+                const float2 ml = __ldcg(
+                    reinterpret_cast<const float2*>(a.part_ml + slot_row(x0 + lane, rr) * 2));
+                f = ex2_ftz(ml.x - ref);
+                fl = ml.y * f;
+              }
+              L += warp_sum(fl);
+              const int n = min(32, c1 - x0 + 1);
+#pragma unroll 8
+              for (int i = 0; i < n; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+                const float* src = a.part_o + slot_row(x0 + i, rr) * HD + lane * V;
+                if (V == 4) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                  acc[0] += v.x * g;
+                  acc[1] += v.y * g;
+                  acc[V - 2] += v.z * g;
+                  acc[V - 1] += v.w * g;
+                } else {
+                  const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                  acc[0] += v.x * g;
+                  acc[1] += v.y * g;
+                }
+              }
             }
             const float inv = L == 0.f ? 0.f : 1.f / L;
             const int ti = a.by_g.div(rr), tk = tok0 + ti, hh = w.h * a.G + rr - ti * a.G;
-            uint2 u;
-            u.x = pack2<T>(s.x * inv, s.y * inv);
-            u.y = pack2<T>(s.z * inv, s.w * inv);
-            *reinterpret_cast<uint2*>(outp + (int64_t)(w.q.row0 + tk) * a.out_stride +
-                                      (int64_t)hh * HD + c4) = u;
-            if (a.lse && c4 == 0)
-              a.lse[(int64_t)(w.q.row0 + tk) * a.nq + hh] =
+            T* dst = outp + (int64_t)(q.row0 + tk) * a.out_stride + (int64_t)hh * HD + lane * V;
+#pragma unroll
+            for (int i = 0; i < V; i += 2)
+              *reinterpret_cast<uint32_t*>(dst + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+            if (a.lse && lane == 0)
+              a.lse[(int64_t)(q.row0 + tk) * a.nq + hh] =
                   L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;
           }
         }
         bar_compute();  // s_last is reused
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_empty(seg));
     }
   }
   if (!ok && lane == 0) set_error(a.err, DFLASH_DEV_TIMEOUT);
 }
 
-template <typename T, int HD, int WM>
+template <typename T, int HD>
 int launch_one(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int box,
                cudaStream_t s) {
-  const size_t smem = 1024 + (size_t)kSlots * slot_bytes<HD>() + scratch_bytes<WM>() +
-                      (size_t)a.batch * 8;
+  constexpr int kFixed = 1024 + kSlots * slot_bytes<HD>() + kScratch;
   static SmemLimit limit;
-  if (!limit.raise(reinterpret_cast<const void*>(attn_paged_kernel<T, HD, WM>),
-                   1024 + kSlots * slot_bytes<HD>() + scratch_bytes<WM>() + kAttnMaxBatch * 8))
+  if (!limit.raise(reinterpret_cast<const void*>(attn_paged_kernel<T, HD>),
+                   kFixed + kAttnMaxBatch * 8))
     return DFLASH_ECUDA;
-  const cudaError_t e = launch_pdl(attn_paged_kernel<T, HD, WM>, dim3(attn_paged_ctas()),
-                                   dim3(kThreads), smem, s, 1, tk, tv, a, box);
+  const cudaError_t e =
+      launch_pdl(attn_paged_kernel<T, HD>, dim3(attn_paged_ctas()), dim3(kThreads),
+                 (size_t)kFixed + (size_t)a.batch * 8, s, 1, tk, tv, a, box);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ECUDA;
-}
-
-template <typename T, int HD>
-int launch_rows(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int box,
-                cudaStream_t s) {
-  if (a.tile_rows == 16) return launch_one<T, HD, 1>(a, tk, tv, box, s);
-  if (a.tile_rows == 32) return launch_one<T, HD, 2>(a, tk, tv, box, s);
-  return launch_one<T, HD, 4>(a, tk, tv, box, s);
 }
 
 }  // namespace
@@ -547,10 +629,10 @@ int launch_attn_paged(const PagedAttnArgs& a, int hd, int dtype, cudaStream_t s)
     return DFLASH_ECUDA;
   TimedScope ts(s, TC_ATTN);
   if (dtype == DFLASH_BF16)
-    return hd == 128 ? launch_rows<__nv_bfloat16, 128>(a, tk, tv, box, s)
-                     : launch_rows<__nv_bfloat16, 64>(a, tk, tv, box, s);
-  return hd == 128 ? launch_rows<__half, 128>(a, tk, tv, box, s)
-                   : launch_rows<__half, 64>(a, tk, tv, box, s);
+    return hd == 128 ? launch_one<__nv_bfloat16, 128>(a, tk, tv, box, s)
+                     : launch_one<__nv_bfloat16, 64>(a, tk, tv, box, s);
+  return hd == 128 ? launch_one<__half, 128>(a, tk, tv, box, s)
+                   : launch_one<__half, 64>(a, tk, tv, box, s);
 }
 
 }  // namespace dflash

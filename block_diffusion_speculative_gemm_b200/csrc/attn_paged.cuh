@@ -118,9 +118,10 @@ __device__ __forceinline__ TileRange tile_range(const PagedAttnArgs& a, const At
 }
 
 // What starting and finishing an item takes, in key tiles: about 4500 cycles
-// against 3200 a tile in the tcgen05 kernel.  An 8192-token prompt, whose first
-// items have one tile and whose last ones 64, has an uneven end without it.
-template <int KL> constexpr int kItemUnits = KL > 0 ? 1 : 1;
+// against 3200 a tile in the tcgen05 kernel, 3 tiles of 64 keys in the other one.
+// An 8192-token prompt, whose first items have one tile and whose last ones 64, has
+// an uneven end without it (501 us against 470).
+template <int KL> constexpr int kItemUnits = KL > 0 ? 3 : 1;
 template <int KL> __device__ __forceinline__ int item_units(const TileRange& x) {
   return x.k1 > x.k0 ? x.k1 - x.k0 + kItemUnits<KL> : 0;
 }
@@ -166,6 +167,28 @@ __device__ __forceinline__ bool pages_mapped(const PagedAttnArgs& a, int r, cons
   return !__any_sync(0xffffffffu, bad);
 }
 
+// Units of request r for one kv head, by a warp; items without keys are written
+// here, by one CTA each.
+template <int HD, int KL>
+__device__ long long attn_units(const PagedAttnArgs& a, int r, const AttnReq& q, int lane) {
+  const int nt = attn_tiles(a, q.n);
+  const bool mine = (int)(r % gridDim.x) == (int)blockIdx.x;
+  long long u = 0;
+  for (int t0 = 0; t0 < nt; t0 += 32) {
+    int k = 0;
+    if (t0 + lane < nt) k = item_units<KL>(tile_range<KL>(a, q, t0 + lane));
+    u += k;
+    if (mine) {
+      unsigned e = __ballot_sync(0xffffffffu, t0 + lane < nt && k == 0);
+      if (e && !pages_mapped(a, r, q, lane)) e = 0;
+      for (; e; e &= e - 1) zero_rows<HD>(a, q, t0 + __ffs(e) - 1, lane);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+  return u;
+}
+
 // Largest batch of a call: the prefix sums of every request sit in shared memory.
 constexpr int kAttnMaxBatch = 4096;
 
@@ -204,24 +227,7 @@ __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
       if (pre[r] >= 0) continue;
       AttnReq q;
       attn_req(a, r, q);
-      const int nt = attn_tiles(a, q.n);
-      const bool mine = (int)(r % gridDim.x) == (int)blockIdx.x;
-      long long u = 0;
-      for (int t0 = 0; t0 < nt; t0 += 32) {
-        int k = 0;
-        if (t0 + lane < nt) {
-          const TileRange x = tile_range<KL>(a, q, t0 + lane);
-          k = item_units<KL>(x);
-        }
-        u += k;
-        if (mine) {
-          unsigned e = __ballot_sync(0xffffffffu, t0 + lane < nt && k == 0);
-          if (e && !pages_mapped(a, r, q, lane)) e = 0;
-          for (; e; e &= e - 1) zero_rows<HD>(a, q, t0 + __ffs(e) - 1, lane);
-        }
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+      const long long u = attn_units<HD, KL>(a, r, q, lane);
       __syncwarp();
       if (lane == 0) pre[r] = u;
     }
@@ -243,6 +249,49 @@ __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
     }
   }
   __syncthreads();
+}
+
+// The same for at most 32 requests, by one warp without a barrier: a lane a
+// request.  Only the warp that walks needs the result.
+template <int HD, int KL>
+__device__ void attn_plan_warp(const PagedAttnArgs& a, long long* pre) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kFew = 4;
+  AttnReq q = {0, 0, 0, 0};
+  long long u = 0;
+  bool spread = false;
+  if (lane < a.batch) {
+    const int bad = attn_req(a, lane, q);
+    if (bad) {
+      if ((int)(lane % gridDim.x) == (int)blockIdx.x) set_error(a.err, bad);
+    } else {
+      const int nt = attn_tiles(a, q.n);
+      spread = nt > kFew;
+      for (int t = 0; t < min(nt, kFew); ++t) {
+        const TileRange x = tile_range<KL>(a, q, t);
+        u += item_units<KL>(x);
+        spread |= x.k1 == x.k0;
+      }
+    }
+  }
+  for (unsigned todo = __ballot_sync(0xffffffffu, spread); todo; todo &= todo - 1) {
+    const int r = __ffs(todo) - 1;
+    AttnReq o;
+    o.row0 = __shfl_sync(0xffffffffu, q.row0, r);
+    o.n = __shfl_sync(0xffffffffu, q.n, r);
+    o.st = __shfl_sync(0xffffffffu, q.st, r);
+    o.len = __shfl_sync(0xffffffffu, q.len, r);
+    const long long v = attn_units<HD, KL>(a, r, o, lane);
+    if (lane == r) u = v;
+  }
+  u *= a.nkv;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long w = __shfl_up_sync(0xffffffffu, u, d);
+    if (lane >= d) u += w;
+  }
+  if (lane < a.batch) pre[lane] = u;
+  __syncwarp();
 }
 
 // The division of W units over N CTAs: the first W % N ranges have one unit more

@@ -381,10 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&fx.tmem), 512);
     tmem_relinquish();
   }
+  if (tid < 3) tma_prefetch_desc(tid == 0 ? &tmQ : tid == 1 ? &tmK : &tmV);
   pdl_wait();
   if (tid == 0) join[blockIdx.x].valid = 0;
   tc_fence_before();
-  attn_plan<HD, 0>(a, pre);  // ends with a barrier
+  if (a.batch > 32)
+    attn_plan<HD, 0>(a, pre);  // ends with a barrier
+  else
+    __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they start at 0
 
@@ -419,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int checked = -1, k = 0;
       bool mapped = false;
       if (ok) {
+        if (a.batch <= 32) attn_plan_warp<HD, 0>(a, pre);
         AttnWalk<0> w(a, pre);
         for (;; ++k) {
           if (k >= kSegs && !wait_warp(seg_empty(k), phase(k - kSegs))) { ok = false; break; }
