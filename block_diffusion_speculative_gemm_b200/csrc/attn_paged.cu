@@ -33,7 +33,8 @@ constexpr int kSlots = 6;                 // ring slots, each a K or a V tile
 constexpr int kPassCols = 64;             // O columns joined at a time
 
 template <int HD> constexpr int slot_bytes() { return kKT * HD * 2; }
-constexpr int kScratch = 3 * 16 * kPassCols * 4;
+constexpr int kPassRow = kPassCols + 8;   // eight rows side by side meet no bank twice
+constexpr int kScratch = 3 * 16 * kPassRow * 4;
 constexpr int kSegs = 4;                  // segments described ahead
 
 // A segment of the CTA's work, as the producer describes it.
@@ -42,7 +43,10 @@ struct Seg {
   int r, h, row0, st, n, len;
   int tok0, tokens;
   int kbeg, kend, whole;
-  int slot, c0, c1, late;  // partial slot; CTAs that share the item, its place in c0
+  int slot;               // partial slot
+  // known by seg_info: the request's pages are mapped; the CTAs that share the item,
+  // its place in c0
+  int mapped, c0, c1, late;
 };
 
 template <typename T>
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                              ~uintptr_t(1023));
   float* scratch = reinterpret_cast<float*>(smem + kSlots * kSlot);
   long long* pre = reinterpret_cast<long long*>(smem + kSlots * kSlot + kScratch);
-  __shared__ __align__(8) uint64_t bars[2 * kSlots + 2 * kSegs];
+  __shared__ __align__(8) uint64_t bars[2 * kSlots + 3 * kSegs];
   __shared__ Seg segs[kSegs];
   __shared__ float s_ml[4][16][2];
   __shared__ int s_abort, s_last;
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto empty = [&](int s) { return smem_u32(&bars[kSlots + s]); };
   auto seg_full = [&](int k) { return smem_u32(&bars[2 * kSlots + k % kSegs]); };
   auto seg_empty = [&](int k) { return smem_u32(&bars[2 * kSlots + kSegs + k % kSegs]); };
+  auto seg_info = [&](int k) { return smem_u32(&bars[2 * kSlots + 2 * kSegs + k % kSegs]); };
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(full(s), 1);
@@ -128,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int k = 0; k < kSegs; ++k) {
       mbar_init(seg_full(k), 1);
       mbar_init(seg_empty(k), 4);
+      mbar_init(seg_info(k), 1);
     }
     fence_barrier_init();
     s_abort = 0;
@@ -157,6 +163,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t pol = policy_evict_first();
     const int per = kKT / box;  // boxes per tile
     int it = 0;                 // ring position
+    int checked = -1;
+    bool mapped = false;
     if (a.batch <= 32) attn_plan_warp<HD, kKL>(a, pre);
     AttnWalk<kKL> w(a, pre);
     for (int k = 0; ok; w.next(), ++k) {
@@ -177,7 +185,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       int ent = 0, ent_base = -1;
       auto describe = [&]() {
         const bool whole = w.whole();
-        const int c0 = whole ? 0 : w.cta_first(), c1 = whole ? 0 : w.cta_last();
         if (lane == 0) {
           d.more = 1;
           d.r = w.r;
@@ -192,10 +199,24 @@ __global__ void __launch_bounds__(kThreads, 2)
           d.kend = w.kend;
           d.whole = whole;
           d.slot = w.slot();
-          d.c0 = c0;
-          d.c1 = c1;
-          d.late = whole ? 0 : w.later_in(c0);
           mbar_arrive(seg_full(k));
+        }
+        __syncwarp();
+        // what takes longer and is needed at the end of the segment only
+        if (w.r != checked) {
+          checked = w.r;
+          mapped = pages_mapped(a, w.r, w.q, lane);
+          if (!mapped && lane == 0) set_error(a.err, DFLASH_DEV_PAGE);
+        }
+        if (lane == 0) {
+          d.mapped = mapped;
+          if (!whole) {
+            const int c0 = w.cta_first();
+            d.c0 = c0;
+            d.c1 = w.cta_last();
+            d.late = w.later_in(c0);
+          }
+          mbar_arrive(seg_info(k));
         }
         __syncwarp();
       };
@@ -248,8 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ldmatrix addresses: K rows are keys (operand as stored), V transposed
     const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
     const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
-    int it = 0, checked = -1;
-    bool mapped = false;
+    int it = 0;
     for (int seg = 0;; ++seg) {
       // a wait that gave up ends all compute warps together, at the next meeting
       ok = __all_sync(0xffffffffu, wait(seg_full(seg), (uint32_t)(seg / kSegs) & 1));
@@ -260,11 +280,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Seg& w = segs[seg % kSegs];
       if (!w.more) break;
       const AttnReq q = {w.row0, w.n, w.st, w.len};
-      if (w.r != checked) {
-        checked = w.r;
-        mapped = pages_mapped(a, w.r, q, lane);
-        if (!mapped && lane == 0) set_error(a.err, DFLASH_DEV_PAGE);
-      }
       const int tok0 = w.tok0, R = w.tokens * a.G, kbeg = w.kbeg, kend = w.kend;
       // this thread's two rows: token, query head within the group
       int row[2], tok[2], hg[2], lo[2], hi[2];
@@ -397,10 +412,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // ---------------------------------------------------------- end of a segment
       // a wait that gave up ends all compute warps here, together
+      ok = ok && __all_sync(0xffffffffu, wait(seg_info(seg), (uint32_t)(seg / kSegs) & 1));
       if (bar_compute_or(!ok)) {
         ok = false;
         break;
       }
+      const bool mapped = w.mapped;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
@@ -436,25 +453,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int pass = 0; pass < HD / kPassCols; ++pass) {
           constexpr int kB = kPassCols / 8;
           if (wk > 0) {
-            float* dst = scratch + (size_t)(wk - 1) * 16 * kPassCols;
+            float* dst = scratch + (wk - 1) * 16 * kPassRow;
 #pragma unroll
             for (int i = 0; i < kB; ++i)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<float2*>(dst + (g8 + 8 * j) * kPassCols + i * 8 + t2) =
-                    make_float2(o[pass * kB + i][2 * j], o[pass * kB + i][2 * j + 1]);
+                if (row[j] < R)
+                  *reinterpret_cast<float2*>(dst + (g8 + 8 * j) * kPassRow + i * 8 + t2) =
+                      make_float2(o[pass * kB + i][2 * j], o[pass * kB + i][2 * j + 1]);
           }
           bar_compute();
           if (wk == 0) {
 #pragma unroll
             for (int k = 1; k < NK; ++k) {
-              const float* src = scratch + (size_t)(k - 1) * 16 * kPassCols;
+              const float* src = scratch + (k - 1) * 16 * kPassRow;
 #pragma unroll
               for (int i = 0; i < kB; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
+                  if (row[j] >= R) continue;
                   const float2 v = *reinterpret_cast<const float2*>(
-                      src + (g8 + 8 * j) * kPassCols + i * 8 + t2);
+                      src + (g8 + 8 * j) * kPassRow + i * 8 + t2);
                   o[pass * kB + i][2 * j] += v.x;
                   o[pass * kB + i][2 * j + 1] += v.y;
                 }
@@ -545,40 +564,45 @@ __global__ void __launch_bounds__(kThreads, 2)
           // a warp a row: the lanes take the partials' maxima and sums side by side,
           // then columns
           for (int rr = warp; rr < R; rr += 4) {
-            float M = -INFINITY;
-            for (int x = c0 + lane; x <= c1; x += 32)
-              M = fmaxf(M, __ldcg(a.part_ml + slot_row(x, rr) * 2));
+            constexpr int V = HD / 32, B = 16;
+            float v[B][V];  // sixteen partials on their way at once
+            auto fetch = [&](int x0) {
+#pragma unroll
+              for (int i = 0; i < B; ++i) {
+                const float* src = a.part_o + slot_row(min(x0 + i, c1), rr) * HD + lane * V;
+                if constexpr (V == 4)
+                  *reinterpret_cast<float4*>(v[i]) = __ldcg(reinterpret_cast<const float4*>(src));
+                else
+                  *reinterpret_cast<float2*>(v[i]) = __ldcg(reinterpret_cast<const float2*>(src));
+              }
+            };
+            auto stats = [&](int x) {
+              return x <= c1 ? __ldcg(reinterpret_cast<const float2*>(a.part_ml +
+                                                                      slot_row(x, rr) * 2))
+                             : make_float2(-INFINITY, 0.f);
+            };
+            float2 ml = stats(c0 + lane);
+            fetch(c0);
+            float M = ml.x;
+            for (int x0 = c0 + 32; x0 <= c1; x0 += 32) M = fmaxf(M, stats(x0 + lane).x);
             M = warp_max(M);
             const float ref = M == -INFINITY ? 0.f : M;
-            constexpr int V = HD / 32;
             float L = 0.f, acc[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = 0.f;
-            for (int x0 = c0; x0 <= c1; x0 += 32) {
-              float f = 0.f, fl = 0.f;
-              if (x0 + lane <= c1) {
-                const float2 ml = __ldcg(
-                    reinterpret_cast<const float2*>(a.part_ml + slot_row(x0 + lane, rr) * 2));
-                f = ex2_ftz(ml.x - ref);
-                fl = ml.y * f;
+            for (int x0 = c0; x0 <= c1; x0 += B) {
+              if (x0 > c0) {
+                if (((x0 - c0) & 31) == 0) ml = stats(x0 + lane);
+                fetch(x0);
               }
-              L += warp_sum(fl);
-              const int n = min(32, c1 - x0 + 1);
-#pragma unroll 8
-              for (int i = 0; i < n; ++i) {
-                const float g = __shfl_sync(0xffffffffu, f, i);
-                const float* src = a.part_o + slot_row(x0 + i, rr) * HD + lane * V;
-                if (V == 4) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                  acc[0] += v.x * g;
-                  acc[1] += v.y * g;
-                  acc[V - 2] += v.z * g;
-                  acc[V - 1] += v.w * g;
-                } else {
-                  const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                  acc[0] += v.x * g;
-                  acc[1] += v.y * g;
-                }
+              const float f = ex2_ftz(ml.x - ref);
+              if (((x0 - c0) & 31) == 0) L += warp_sum(ml.y * f);
+#pragma unroll
+              for (int i = 0; i < B; ++i) {
+                const float g = __shfl_sync(0xffffffffu, f, ((x0 - c0) & 31) + i);
+                if (x0 + i > c1) continue;
+#pragma unroll
+                for (int d = 0; d < V; ++d) acc[d] += v[i][d] * g;
               }
             }
             const float inv = L == 0.f ? 0.f : 1.f / L;
