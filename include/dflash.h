@@ -527,8 +527,8 @@ size_t dflash_attention_paged_workspace_size(int batch, int n_rows, int n_q, int
  *   lse      device fp32 [n_rows][n_q] out or NULL: ln sum_j w_j
  * Keys that no row of a request sees are never used, whatever their slots hold
  * (NaN included), and their pages need not be mapped; a key that only some rows
- * see does not reach the others.  scale > 0; n_q / n_kv <= 64, batch <= 4096
- * (DFLASH_EUNSUPPORTED beyond).  The same inputs give the same bits; how a
+ * see does not reach the others.  scale > 0; n_q / n_kv <= 64, batch <= 4096,
+ * n_rows <= 2^30 (DFLASH_EUNSUPPORTED beyond).  The same inputs give the same bits; how a
  * request's keys are divided over the GPU depends on the whole batch, so its
  * rows can change at rounding level when the other requests change. */
 int dflash_attention_paged(const void* q, int64_t q_stride, int dtype, const int32_t* cu_rows,
