@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 4) {
     // ------------------------------------------------------------ producer
     const uint64_t pol = policy_evict_first();
-    const int per = kKT / box;  // boxes per tile
+    const int per = kKT / box, per_log2 = __ffs(per) - 1;  // boxes a tile, at most 4
     int it = 0;                 // ring position
     int checked = -1;
     bool mapped = false;
@@ -182,7 +182,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         break;
       }
       const int32_t* tab = a.table + (int64_t)w.r * a.max_pages;
-      int ent = 0, ent_base = -1;
+      // the pool rows of the segment's boxes b0 .. b0 + 31, a lane each
+      auto lookup = [&](int b0) -> int {
+        const int key = w.kbeg * kKT + (b0 + lane) * box;
+        int y = rows_all;
+        if (key < w.q.len && b0 < (w.kend - w.kbeg) * per) {
+          const int pg = a.by_page.div(key), e = tab[pg];
+          if (e >= 0 && e < a.n_pages) y = (e * a.nkv + w.h) * a.page + key - pg * a.page;
+        }
+        if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
+        return y;
+      };
+      int ent = lookup(0), ahead = lookup(32);  // these boxes, the next ones
       auto describe = [&]() {
         const bool whole = w.whole();
         if (lane == 0) {
@@ -221,18 +232,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
       };
       for (int kt = w.kbeg; kt < w.kend && ok; ++kt) {
-        // the pool rows of the tile's boxes, looked up 32 boxes at a time
-        const int b0 = (kt - w.kbeg) * per;
-        if (ent_base < 0 || b0 + per > ent_base + 32) {
-          ent_base = b0;
-          const int key = w.kbeg * kKT + (b0 + lane) * box;
-          int y = rows_all;
-          if (key < w.q.len) {
-            const int pg = a.by_page.div(key), e = tab[pg];
-            if (e >= 0 && e < a.n_pages) y = (e * a.nkv + w.h) * a.page + key - pg * a.page;
-          }
-          if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
-          ent = y;
+        const int b0 = ((kt - w.kbeg) * per) & 31;  // a tile's boxes divide 32
+        if (kt > w.kbeg && b0 == 0) {
+          ent = ahead;
+          ahead = lookup((kt - w.kbeg) * per + 32);
         }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++it) {
@@ -246,15 +249,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (lane == 0) mbar_arrive_expect_tx(full(s), kSlot);
           __syncwarp();
-          for (int b = 0; b < per; ++b) {
-            const int y = __shfl_sync(0xffffffffu, ent, b0 + b - ent_base);
-            if (lane == 0) {
-              const uint32_t dst = s_base + s * kSlot + b * box * 128;
-#pragma unroll
-              for (int hf = 0; hf < HD / 64; ++hf)
-                tma_load_2d(dst + hf * kHalfTile, kv ? &tmV : &tmK, full(s), hf * 64, y, pol);
-            }
-          }
+          // the tile's boxes side by side, a lane each
+          const int hf = lane >> per_log2, b = lane & (per - 1);
+          const int y = __shfl_sync(0xffffffffu, ent, b0 + b);
+          if (hf < HD / 64)
+            tma_load_2d(s_base + s * kSlot + b * box * 128 + hf * kHalfTile, kv ? &tmV : &tmK,
+                        full(s), hf * 64, y, pol);
           if (kt == w.kbeg && kv == 1 && it < kSlots) describe();
         }
       }

@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kTmaWarp) {
       // ---------------------------------------------------------- TMA
       const int rows_all = a.n_pages * a.nkv * a.page;  // past the pools: TMA fills zeros
-      const int per = kKT / box;
+      const int per = kKT / box, per_log2 = __ffs(per) - 1;  // boxes a tile, at most 8
       RingPos at;
       int it = 0, k = 0;  // tiles asked for, segments
       for (; ok; ++k) {
@@ -491,21 +491,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys that one query tile reads pass through once
         const uint64_t pol = g.two ? policy_evict_last() : policy_evict_first();
         const int32_t* tab = a.table + (int64_t)g.r * a.max_pages;
-        int ent = 0, ent_base = -1;
-        const int quad = g.two ? 1 : 2;  // runs per step
+        // the pool rows of the segment's boxes b0 .. b0 + 31, a lane each
+        auto lookup = [&](int b0) -> int {
+          const int key = g.run0 * kKT + (b0 + lane) * box;
+          int y = rows_all;
+          if (key < g.len && b0 < g.runs * per) {
+            const int pg = a.by_page.div(key), e = tab[pg];
+            if (e >= 0 && e < a.n_pages) y = (e * a.nkv + g.h) * a.page + key - pg * a.page;
+          }
+          if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
+          return y;
+        };
+        int ent = lookup(0), ahead = lookup(32);  // these boxes, the next ones
+        const int quad = g.two ? 1 : 2;  // runs per step; a step's boxes divide 32
         for (int j = 0; j < g.runs && ok; j += quad) {
-          // the pool rows of the step's boxes, looked up 32 boxes at a time
-          const int b0 = j * per;
-          if (ent_base < 0 || b0 + quad * per > ent_base + 32) {
-            ent_base = b0;
-            const int key = g.run0 * kKT + (b0 + lane) * box;
-            int y = rows_all;
-            if (key < g.len) {
-              const int pg = a.by_page.div(key), e = tab[pg];
-              if (e >= 0 && e < a.n_pages) y = (e * a.nkv + g.h) * a.page + key - pg * a.page;
-            }
-            if (!DFLASH_CHECK(y >= 0 && y <= rows_all, a.err)) y = rows_all;
-            ent = y;
+          const int b0 = (j * per) & 31;
+          if (j > 0 && b0 == 0) {
+            ent = ahead;
+            ahead = lookup(j * per + 32);
           }
           const int nr = min(quad, g.runs - j);
           for (int o = 0; o < 2 * nr; ++o, ++it) {  // K of the step's runs, then V
@@ -518,12 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             at.next(slots);
             if (lane == 0) mbar_arrive_expect_tx(full(s), kTile);
             __syncwarp();
-            for (int b = 0; b < per; ++b) {
-              const int y = __shfl_sync(0xffffffffu, ent, b0 + run * per + b - ent_base);
-              if (lane < kHalves)
-                tma_load_2d(s_ring + s * kTile + b * box * 128 + lane * kHalfTile,
-                            kv ? &tmV : &tmK, full(s), lane * 64, y, pol);
-            }
+            // the tile's boxes side by side, a lane each
+            const int hf = lane >> per_log2, b = lane & (per - 1);
+            const int y = __shfl_sync(0xffffffffu, ent, b0 + run * per + b);
+            if (hf < kHalves)
+              tma_load_2d(s_ring + s * kTile + b * box * 128 + hf * kHalfTile, kv ? &tmV : &tmK,
+                          full(s), hf * 64, y, pol);
             if (j == 0 && o == 0) {
               // the item's queries, behind its first keys: the last products of the
               // segment before release the buffer
