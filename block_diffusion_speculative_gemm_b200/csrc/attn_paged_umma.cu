@@ -883,7 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partials of the items that several CTAs shared: block (c, y) does
 // rows [32 y, 32 y + 32) of the item that begins in CTA c's range, 8 threads a
-// row, its pieces in CTA order.
+// row, its pieces in CTA order, four on their way at once: what it costs is the
+// latency of its loads.
 template <typename T, int HD>
 __global__ void __launch_bounds__(256)
     attn_join_kernel(const __grid_constant__ PagedAttnArgs a, const JoinItem* join) {
@@ -899,27 +900,49 @@ __global__ void __launch_bounds__(256)
   auto at = [&](int cta) {
     return (size_t)(2 * cta + (cta == c0 ? d.late : 0)) * a.tile_rows + row;
   };
-  float M = -INFINITY;
-  for (int cta = c0; cta <= d.last; ++cta) M = fmaxf(M, __ldcg(a.part_ml + at(cta) * 2));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  constexpr int V = HD / 32;  // float4 a thread: columns 4 (sub + 8 i)
+  float M = -INFINITY, ref = 0.f, L = 0.f;
+  constexpr int V = HD / 32, B = 4;  // float4 a thread: columns 4 (sub + 8 i); pieces at a time
   float4 acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int cta = c0; cta <= d.last; ++cta) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at(cta) * 2));
-    const float f = ex2_ftz(ml.x - ref);
-    L += ml.y * f;
-    const float4* src = reinterpret_cast<const float4*>(a.part_o + at(cta) * HD) + sub;
+  for (int cta = c0; cta <= d.last; cta += B) {
+    float2 ml[B];
+    float4 v[B][V];
+#pragma unroll
+    for (int e = 0; e < B; ++e) {
+      ml[e] = make_float2(-INFINITY, 0.f);
+      if (cta + e > d.last) continue;
+      const size_t from = at(cta + e);
+      ml[e] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + from * 2));
+      const float4* src = reinterpret_cast<const float4*>(a.part_o + from * HD) + sub;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[e][i] = __ldcg(src + 8 * i);
+    }
+    const float before = M;
+#pragma unroll
+    for (int e = 0; e < B; ++e) M = fmaxf(M, ml[e].x);
+    ref = M == -INFINITY ? 0.f : M;
+    const float g = ex2_ftz(before - ref);
+    L *= g;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float4 v = __ldcg(src + 8 * i);
-      acc[i].x += v.x * f;
-      acc[i].y += v.y * f;
-      acc[i].z += v.z * f;
-      acc[i].w += v.w * f;
+      acc[i].x *= g;
+      acc[i].y *= g;
+      acc[i].z *= g;
+      acc[i].w *= g;
+    }
+#pragma unroll
+    for (int e = 0; e < B; ++e) {
+      if (cta + e > d.last) continue;
+      const float f = ex2_ftz(ml[e].x - ref);
+      L += ml[e].y * f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        acc[i].x += v[e][i].x * f;
+        acc[i].y += v[e][i].y * f;
+        acc[i].z += v[e][i].z * f;
+        acc[i].w += v[e][i].w * f;
+      }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
