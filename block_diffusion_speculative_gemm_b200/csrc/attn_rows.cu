@@ -80,6 +80,54 @@ __device__ __forceinline__ bool put8<float>(float* dst, const float (&v)[8]) {
   return false;
 }
 
+// A lane's part of a head in pairs: 8 values of each half.  Both kernels use the
+// same steps, so that a row's bits do not depend on which of them takes it.
+struct HeadPart {
+  uint64_t a[4], b[4];
+  __device__ __forceinline__ void set(const float (&y1)[8], const float (&y2)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = pair(y1[2 * k], y1[2 * k + 1]);
+      b[k] = pair(y2[2 * k], y2[2 * k + 1]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&y1)[8], float (&y2)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      unpair(a[k], y1[2 * k], y1[2 * k + 1]);
+      unpair(b[k], y2[2 * k], y2[2 * k + 1]);
+    }
+  }
+  __device__ __forceinline__ float sum_of_squares() const {
+    uint64_t q = mul2(a[0], a[0]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) q = fma2(a[k], a[k], q);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q = fma2(b[k], b[k], q);
+    float s0, s1;
+    unpair(q, s0, s1);
+    return s0 + s1;
+  }
+  __device__ __forceinline__ void scale(float inv, const uint64_t (&g)[8]) {
+    const uint64_t f = pair(inv, inv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = mul2(mul2(a[k], f), g[k]);
+      b[k] = mul2(mul2(b[k], f), g[4 + k]);
+    }
+  }
+  // cs, sn: cosines and sines in pairs
+  __device__ __forceinline__ void rotate(const uint64_t (&cs)[4], const uint64_t (&sn)[4]) {
+    const uint64_t minus = pair(-1.f, -1.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t u = a[k];
+      a[k] = fma2(u, cs[k], mul2(mul2(b[k], minus), sn[k]));
+      b[k] = fma2(b[k], cs[k], mul2(u, sn[k]));
+    }
+  }
+};
+
 // What a warp learns about a row: its request's rows and first position.
 struct RowOwner {
   int req, row0, n, st;
@@ -183,14 +231,20 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowArgs p) {
     return;
   }
   const int pos = o.st + (row - o.row0);
-  float cs[8], sn[8];
+  uint64_t cs[4], sn[4];
   if (p.rope) {
     const float* t = p.rope + (int64_t)pos * kHalf + i0;
     Raw8<float> c, s;
     c.load(t);
     s.load(t + (int64_t)p.max_pos * kHalf);
-    c.get(cs);
-    s.get(sn);
+    float cv[8], sv[8];
+    c.get(cv);
+    s.get(sv);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      cs[k] = pair(cv[2 * k], cv[2 * k + 1]);
+      sn[k] = pair(sv[2 * k], sv[2 * k + 1]);
+    }
   }
   int64_t slot = 0;  // paged: pool row of head 0
   if (kPaged) {
@@ -216,41 +270,34 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowArgs p) {
       // every lane of the warp takes the shuffles; h is uniform over a group's lanes
       const bool live = h < nh, is_a = h < p.n_a;
       float y1[8], y2[8];
+      HeadPart y;
       if (live) {
         x[u][0].get(y1);
         x[u][1].get(y2);
+        y.set(y1, y2);
       }
       const TI* g = static_cast<const TI*>(is_a ? p.g_a : p.g_b);
       if (p.g_a != nullptr || p.g_b != nullptr) {
-        float ss = 0.f;
-        if (live)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss += y1[i] * y1[i] + y2[i] * y2[i];
+        float ss = live ? y.sum_of_squares() : 0.f;
 #pragma unroll
         for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
         if (live && g != nullptr) {
-          const float inv = rsqrtf(ss / HD + p.eps);
           Raw8<TI> gr;
           float gv[8];
-          gr.load(g + i0);
-          gr.get(gv);
+          uint64_t g2[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y1[i] = y1[i] * inv * gv[i];
-          gr.load(g + i0 + kHalf);
-          gr.get(gv);
+          for (int half = 0; half < 2; ++half) {
+            gr.load(g + half * kHalf + i0);
+            gr.get(gv);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y2[i] = y2[i] * inv * gv[i];
+            for (int k = 0; k < 4; ++k) g2[half * 4 + k] = pair(gv[2 * k], gv[2 * k + 1]);
+          }
+          y.scale(rsqrtf(ss / HD + p.eps), g2);
         }
       }
       if (!live) continue;
-      if (p.rope && (is_a || !kPaged)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = y1[i], b = y2[i];
-          y1[i] = a * cs[i] - b * sn[i];
-          y2[i] = b * cs[i] + a * sn[i];
-        }
-      }
+      if (p.rope && (is_a || !kPaged)) y.rotate(cs, sn);
+      y.get(y1, y2);
       TO* dst;
       if (kPaged) {
         const int64_t d = slot + (int64_t)(is_a ? h : h - p.n_a) * p.page;
@@ -442,8 +489,8 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
   } else {
     // ------------------------------------------------------------ rows
     const int i0 = (lane % kLanes) * 8, hg = lane / kLanes;
-    float ga[16], gb[16];
-    auto gains = [&](const void* g, float (&v)[16]) {
+    uint64_t ga[8], gb[8];  // gains of this lane's columns, in pairs
+    auto gains = [&](const void* g, uint64_t (&v)[8]) {
       Raw8<TI> r;
       float t[8];
 #pragma unroll
@@ -453,7 +500,8 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
           r.get(t);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[half * 8 + i] = g != nullptr ? t[i] : 1.f;
+        for (int i = 0; i < 4; ++i)
+          v[half * 4 + i] = g != nullptr ? pair(t[2 * i], t[2 * i + 1]) : pair(1.f, 1.f);
       }
     };
     gains(p.g_a, ga);
@@ -468,16 +516,16 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
       const int64_t row = info[s].row, slot = info[s].slot;
       if (row >= 0) {
         const uint8_t* x = smem + s * stage;
-        float cs[8], sn[8];
+        uint64_t cs[4], sn[4];
         if (p.rope) {
-          const float* t = reinterpret_cast<const float*>(x + nh * HD * sizeof(TI));
-          Raw8<float> c;
-          c.a = reinterpret_cast<const float4*>(t + i0)[0];
-          c.b = reinterpret_cast<const float4*>(t + i0)[1];
-          c.get(cs);
-          c.a = reinterpret_cast<const float4*>(t + kHalf + i0)[0];
-          c.b = reinterpret_cast<const float4*>(t + kHalf + i0)[1];
-          c.get(sn);
+          const float* t = reinterpret_cast<const float*>(x + nh * HD * sizeof(TI)) + i0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 c = *reinterpret_cast<const float2*>(t + 2 * k);
+            const float2 v = *reinterpret_cast<const float2*>(t + kHalf + 2 * k);
+            cs[k] = pair(c.x, c.y);
+            sn[k] = pair(v.x, v.y);
+          }
         }
 #pragma unroll 1
         for (int h0 = 0; h0 < nh; h0 += kHeads) {
@@ -487,30 +535,20 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
           const TI* src = reinterpret_cast<const TI*>(x) + min(h, nh - 1) * HD + i0;
           lds8(src, y1);
           lds8(src + kHalf, y2);
+          HeadPart y;
+          y.set(y1, y2);
           if (p.g_a != nullptr || (!kPaged && p.g_b != nullptr)) {
-            float ss = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ss += y1[k] * y1[k] + y2[k] * y2[k];
+            float ss = y.sum_of_squares();
 #pragma unroll
             for (int d = kLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
             if (is_a ? p.g_a != nullptr : !kPaged && p.g_b != nullptr) {
               const float inv = rsqrtf(ss / HD + p.eps);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                y1[k] = y1[k] * inv * (is_a || kPaged ? ga[k] : gb[k]);
-                y2[k] = y2[k] * inv * (is_a || kPaged ? ga[8 + k] : gb[8 + k]);
-              }
+              if (is_a || kPaged) y.scale(inv, ga); else y.scale(inv, gb);
             }
           }
           if (!live) continue;
-          if (p.rope && (is_a || !kPaged)) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float a = y1[k], b = y2[k];
-              y1[k] = a * cs[k] - b * sn[k];
-              y2[k] = b * cs[k] + a * sn[k];
-            }
-          }
+          if (p.rope && (is_a || !kPaged)) y.rotate(cs, sn);
+          y.get(y1, y2);
           TO* dst;
           if (kPaged) {
             const int64_t d = slot + (int64_t)(is_a ? h : h - p.n_a) * p.page;
