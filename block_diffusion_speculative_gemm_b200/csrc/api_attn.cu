@@ -54,9 +54,10 @@ int check_pool(const void* k_pool, const void* v_pool, int cache_dtype, int n_kv
 
 // Rows of an item tile: the average request's rows decide.  Any tile is right
 // for any mix of lengths; 256 is the tcgen05 kernel's pair of query tiles.  With
-// 16 rows (32 requests of one token, 4 query heads a key head) the mma.sync
-// kernel takes 53 us and the tcgen05 kernel 55; with 32 rows (blocks of 8) the
-// former took 67 and the latter takes 56, with 64 rows 172 and 96.
+// 4 rows (32 requests of one token, 4 query heads a key head) the mma.sync kernel
+// takes 49 us and the tcgen05 kernel 53, one request of one token 12 and 17; with
+// 32 rows (blocks of 8) the former took 67 and the latter takes 53, with 64 rows
+// 172 and 93.
 int pick_tile_rows(int batch, int n_rows, int G) {
   const int64_t rows = std::max<int64_t>(((int64_t)n_rows + batch - 1) / batch * G, G);
   return rows <= 16 ? 16 : 256;
