@@ -144,6 +144,22 @@ def test_many_requests(batch, rows, hd):
     c.check(*c.run(True, 33), True, 33)
 
 
+@pytest.mark.parametrize("rows", [1, 7])
+def test_the_largest_batch(rows):
+    # 4096 requests, most of them with a few rows, some with none, some without keys
+    n = [rows if k % 9 else 0 for k in range(4096)]
+    ctx = [k % 23 for k in range(4096)]
+    c = Case(77, n, ctx, 4, 1, 64, "f16", 16, kv_len=[a + b if k % 13 else 0 for k, (a, b) in
+                                                      enumerate(zip(n, ctx))])
+    c.check(*c.run())
+    with pytest.raises(D.DFlashError):
+        ws = D.attention_paged_workspace(1, 1, 4, 1, 64)
+        e = torch.zeros(4097, dtype=torch.int32, device="cuda")
+        D.attention_paged(c.q[:1], torch.zeros(4098, dtype=torch.int32, device="cuda"), e, e, c.kp,
+                          c.vp, torch.zeros(4097, 1, dtype=torch.int32, device="cuda"),
+                          torch.empty_like(c.q[:1]), ws)
+
+
 def test_one_long_chunk_among_single_tokens():
     # the average is far from every request: 40 single tokens and a chunk of 200
     c = Case(72, [1] * 20 + [200] + [1] * 20, [90 * (k % 11) for k in range(41)], 8, 2, 128,
