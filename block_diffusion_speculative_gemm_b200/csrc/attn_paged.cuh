@@ -82,7 +82,7 @@ __device__ __forceinline__ int attn_req(const PagedAttnArgs& a, int r, AttnReq& 
   q.row0 = a.cu[r];
   const int end = a.cu[r + 1];
   q.st = a.start[r];
-  if (q.row0 < 0 || end < q.row0 || end > a.n_rows) return DFLASH_DEV_ROWS;
+  if (out_of_order(q.row0, end, a.n_rows)) return DFLASH_DEV_ROWS;
   q.n = end - q.row0;
   const int64_t last = (int64_t)q.st + q.n;
   const int64_t len = a.kv_len ? (int64_t)a.kv_len[r] : last;
@@ -193,19 +193,21 @@ __device__ long long attn_units(const PagedAttnArgs& a, int r, const AttnReq& q,
 constexpr int kAttnMaxBatch = 4096;
 
 // Fills pre[r] with the units of requests 0..r (every thread of the CTA; ends
-// with a barrier).  Requests with bad lengths have none and set their error
-// bits; items without keys have none and are written here, by one CTA each.
+// with a barrier).  Requests with bad lengths or rows out of order have none and set
+// their error bits; items without keys have none and are written here, by one CTA
+// each.
 template <int HD, int KL>
 __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthr = blockDim.x, nw = nthr >> 5;
   constexpr int kFew = 4;  // item tiles a single thread adds up
-  bool spread = false;
+  bool spread = false, order = true;
   for (int r = tid; r < a.batch; r += nthr) {
     AttnReq q;
     long long u = 0;
     const int bad = attn_req(a, r, q);
     if (bad) {
+      order &= bad != DFLASH_DEV_ROWS;
       if ((int)(r % gridDim.x) == (int)blockIdx.x) set_error(a.err, bad);
     } else {
       const int nt = attn_tiles(a, q.n);
@@ -222,7 +224,17 @@ __device__ void attn_plan(const PagedAttnArgs& a, long long* pre) {
     }
     pre[r] = u;
   }
-  if (__syncthreads_or(spread)) {
+  if (__syncthreads_or(spread || !order)) {
+    if (__syncthreads_or(!order)) {  // the requests that overlap earlier ones
+      if (warp == 0)
+        each_request_order(a.cu, a.batch, a.n_rows, lane, [&](int r, bool ok, int, int) {
+          if (r < a.batch && !ok) {
+            pre[r] = 0;
+            if ((int)(r % gridDim.x) == (int)blockIdx.x) set_error(a.err, DFLASH_DEV_ROWS);
+          }
+        });
+      __syncthreads();
+    }
     for (int r = warp; r < a.batch; r += nw) {
       if (pre[r] >= 0) continue;
       AttnReq q;
@@ -259,10 +271,11 @@ __device__ void attn_plan_warp(const PagedAttnArgs& a, long long* pre) {
   constexpr int kFew = 4;
   AttnReq q = {0, 0, 0, 0};
   long long u = 0;
-  bool spread = false;
+  bool spread = false, order = true;
   if (lane < a.batch) {
     const int bad = attn_req(a, lane, q);
     if (bad) {
+      order = bad != DFLASH_DEV_ROWS;
       if ((int)(lane % gridDim.x) == (int)blockIdx.x) set_error(a.err, bad);
     } else {
       const int nt = attn_tiles(a, q.n);
@@ -274,6 +287,14 @@ __device__ void attn_plan_warp(const PagedAttnArgs& a, long long* pre) {
       }
     }
   }
+  if (!__all_sync(0xffffffffu, order))  // the requests that overlap earlier ones
+    each_request_order(a.cu, a.batch, a.n_rows, lane, [&](int r, bool ok, int, int) {
+      if (r < a.batch && !ok) {
+        u = 0;
+        spread = false;
+        if ((int)(r % gridDim.x) == (int)blockIdx.x) set_error(a.err, DFLASH_DEV_ROWS);
+      }
+    });
   for (unsigned todo = __ballot_sync(0xffffffffu, spread); todo; todo &= todo - 1) {
     const int r = __ffs(todo) - 1;
     AttnReq o;

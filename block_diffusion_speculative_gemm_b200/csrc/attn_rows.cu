@@ -132,17 +132,21 @@ struct HeadPart {
 struct RowOwner {
   int req, row0, n, st;
   int total;  // cu_rows[batch]
+  bool order; // cu_rows ascends inside the rows (as far as this search saw it)
 };
 
 // The request that holds `row` (the last one whose first row is <= row), by a
 // search over 32 probes a round: one round up to 32 requests, two up to 1024.
+// Where cu_rows does not ascend the answer means nothing: owner_in_order has it then.
 __device__ __forceinline__ RowOwner find_owner(const int32_t* cu, const int32_t* start, int batch,
-                                               int row, int lane) {
+                                               int n_rows, int row, int lane) {
   RowOwner o;
+  o.order = true;
   if (batch <= 32) {
     const int l = min(lane, batch - 1);
     const int a = cu[l], b = cu[l + 1], st = start[l];
     const unsigned le = __ballot_sync(0xffffffffu, lane < batch && a <= row);
+    o.order = __all_sync(0xffffffffu, !out_of_order(a, b, n_rows));
     o.req = le ? 31 - __clz(le) : 0;
     o.row0 = __shfl_sync(0xffffffffu, a, o.req);
     o.n = __shfl_sync(0xffffffffu, b, o.req) - o.row0;
@@ -165,6 +169,21 @@ __device__ __forceinline__ RowOwner find_owner(const int32_t* cu, const int32_t*
   o.st = start[lo];
   o.total = cu[batch];
   return o;
+}
+
+// The requests in order that hold the rows [first, first + 32): own(r, a, b) on every
+// lane of the warp for each of them.
+template <typename F>
+__device__ void owners_in_order(const int32_t* cu, int batch, int n_rows, int first, int lane,
+                                F own) {
+  each_request_order(cu, batch, n_rows, lane, [&](int r, bool ok, int a, int b) {
+    for (unsigned hit = __ballot_sync(0xffffffffu, ok && a < first + 32LL && b > first && b > a);
+         hit; hit &= hit - 1) {
+      const int src = __ffs(hit) - 1;
+      own(__shfl_sync(0xffffffffu, r, src), __shfl_sync(0xffffffffu, a, src),
+          __shfl_sync(0xffffffffu, b, src));
+    }
+  });
 }
 
 struct RowArgs {
@@ -196,7 +215,6 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowArgs p) {
   const int grp = tid / kLanes, i0 = (tid % kLanes) * 8;
   const int gpr = 1 << p.groups_log2;  // at least 8, so that a warp's groups share their row
   const int row = blockIdx.x * ((kThreads / kLanes) >> p.groups_log2) + (grp >> p.groups_log2);
-  if (row >= p.n_rows) return;
   const int hg = grp & (gpr - 1);
   const int nh = p.n_a + p.n_b;
 
@@ -214,13 +232,33 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowArgs p) {
       }
     }
   };
-  fetch(hg);  // in flight while the row's request is looked up
+  if (row < p.n_rows) fetch(hg);  // in flight while the row's request is looked up
 
-  const RowOwner o = find_owner(p.cu, p.start, p.batch, row, lane);
-  if (row >= o.total && o.total >= 0) return;  // padding behind the last request
-  if (row < o.row0 || row - o.row0 >= o.n || o.row0 < 0 || o.row0 + (int64_t)o.n > p.n_rows) {
+  RowOwner o = find_owner(p.cu, p.start, p.batch, p.n_rows, row, lane);
+  bool order = o.order;
+  if (p.batch > 32) {  // the search saw a part of cu_rows only
+    for (int r = tid; r < p.batch; r += kThreads)
+      order &= !out_of_order(p.cu[r], p.cu[r + 1], p.n_rows);
+    order = __syncthreads_and(order);
+  }
+  if (row >= p.n_rows) return;
+  if (!order) {
     if (lane == 0) set_error(p.err, DFLASH_DEV_ROWS);
-    return;
+    o.n = 0;
+    owners_in_order(p.cu, p.batch, p.n_rows, row, lane, [&](int r, int a, int b) {
+      if (row < a || row >= b) return;
+      o.req = r;
+      o.row0 = a;
+      o.n = b - a;
+      o.st = p.start[r];
+    });
+    if (o.n == 0) return;
+  } else {
+    if (row >= o.total) return;  // padding behind the last request
+    if (row < o.row0) {          // in front of the first one
+      if (lane == 0) set_error(p.err, DFLASH_DEV_ROWS);
+      return;
+    }
   }
   // the whole request has to fit the table and the cache, else none of its rows is written
   const int64_t last = (int64_t)o.st + o.n - 1;
@@ -372,8 +410,11 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
     }
     fence_barrier_init();
   }
-  __syncthreads();
   pdl_wait();
+  bool order = true;
+  for (int r = tid; r < p.batch; r += blockDim.x)
+    order &= !out_of_order(p.cu[r], p.cu[r + 1], p.n_rows);
+  order = __syncthreads_and(order);
   const int r_begin = (int)((int64_t)p.n_rows * blockIdx.x / gridDim.x);
   const int count = (int)((int64_t)p.n_rows * (blockIdx.x + 1) / gridDim.x) - r_begin;
   bool ok = true;
@@ -381,6 +422,7 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
   if (warp == warps) {
     // ------------------------------------------------------------ loads
     const int total = p.cu[p.batch];
+    if (!order && lane == 0) set_error(p.err, DFLASH_DEV_ROWS);
     int checked = -1;     // the request whose pages were looked through
     bool mapped = true;
     int s = 0, phase = 1;  // stage, parity of its last release (none yet)
@@ -389,8 +431,17 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
       // a row per lane: its request (the last one that starts at or before it)
       const int row = r_begin + i + lane;
       int req = 0, row0 = 0, n = 0, st = 0;
-      bool good = i + lane < count && !(row >= total && total >= 0);
-      if (good) {
+      bool good = i + lane < count && (row < total || !order);
+      if (!order) {
+        owners_in_order(p.cu, p.batch, p.n_rows, r_begin + i, lane, [&](int r, int a, int b) {
+          if (row < a || row >= b) return;
+          req = r;
+          row0 = a;
+          n = b - a;
+          st = p.start[r];
+        });
+        good = good && n > 0;
+      } else if (good) {
         int lo = 0, hi = p.batch - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
@@ -400,7 +451,7 @@ __global__ void __launch_bounds__(kStreamMax / 2 * 32 + 32)
         row0 = p.cu[lo];
         n = p.cu[lo + 1] - row0;
         st = p.start[lo];
-        if (row < row0 || row - row0 >= n || row0 < 0 || row0 + (int64_t)n > p.n_rows) {
+        if (row < row0) {  // in front of the first request
           set_error(p.err, DFLASH_DEV_ROWS);
           good = false;
         }

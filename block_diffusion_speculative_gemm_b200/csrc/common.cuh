@@ -120,6 +120,33 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return warp_sum(t);
 }
 
+// ---------------------------------------------------------------- ragged rows
+// Request r of a ragged call has the rows [cu[r], cu[r+1]).  It is in order when that
+// is an ascending range inside [0, n_rows] and no earlier entry lies above cu[r]; the
+// ranges of requests in order never overlap.  Where no request has out_of_order, every
+// one of them is in order and cu ascends.
+__device__ __forceinline__ bool out_of_order(int a, int b, int n_rows) {
+  return a < 0 || b < a || b > n_rows;
+}
+
+// The order of every request, by a warp, for the calls where one is out of it:
+// f(r, ok, a, b) with a request a lane (ok false behind the last one).
+template <typename F>
+__device__ void each_request_order(const int32_t* cu, int batch, int n_rows, int lane, F f) {
+  int top = 0;  // the largest entry so far
+  for (int r0 = 0; r0 < batch; r0 += 32) {
+    const int r = r0 + lane, a = cu[min(r, batch)], b = cu[min(r + 1, batch)];
+    int most = max(a, top);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, most, d);
+      if (lane >= d) most = max(most, o);
+    }
+    f(r, r < batch && a == most && !out_of_order(a, b, n_rows), a, b);
+    top = __shfl_sync(0xffffffffu, most, 31);
+  }
+}
+
 // ---------------------------------------------------------------- bounded waits
 // Every spin-wait in this library gives up after kWaitNs of wall time, sets
 // DFLASH_DEV_TIMEOUT and lets the kernel run to its exit path.
