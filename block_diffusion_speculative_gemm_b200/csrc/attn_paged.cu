@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ Seg segs[kSegs];
   __shared__ float s_ml[4][16][2];
   __shared__ int s_abort, s_last;
+  __shared__ int s_taken;  // values of the segment were taken out (ItemKeys)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t s_base = smem_u32(smem);
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     fence_barrier_init();
     s_abort = 0;
+    s_taken = 0;
   }
   if (tid < 2) tma_prefetch_desc(tid == 0 ? &tmK : &tmV);
   __syncthreads();
@@ -305,9 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           qf[ks][j + 2] = *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8);
         }
       }
-      // every row of the item sees the keys [all_lo, all_hi)
-      const int all_hi = row_hi(a, q, q.st + tok0);
-      const int all_lo = row_lo(a, q.st + tok0 + w.tokens - 1);
+      const ItemKeys keys(a, q, tok0, w.tokens);
       float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i)
@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(sk));
-        if (key0 < all_lo || key0 + KW > all_hi) {
+        const bool edge = key0 < keys.all_lo || key0 + KW > keys.all_hi;
+        if (edge) {
 #pragma unroll
           for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -377,7 +378,15 @@ __global__ void __launch_bounds__(kThreads, 2)
           break;
         }
         const uint32_t vb = s_base + sv * kSlot + (uint32_t)(wk * KW) * 128;
-        const bool tail = key0 + KW > q.len;
+        if (edge) {
+          const int k0 = kt * kKT;
+          edge_values<T, HD, kKT>(smem + sv * kSlot, wk * KW, wk * KW + KW, keys.lo - k0,
+                                  keys.hi - k0, keys.all_lo - k0, keys.all_hi - k0, lane,
+                                  &s_taken);
+          // the slot's next tile comes by TMA
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
 #pragma unroll
         for (int k2 = 0; k2 < KW / 16; ++k2) {
           // P rounded to the operand type: relative error at most half a step per weight
@@ -385,26 +394,11 @@ __global__ void __launch_bounds__(kThreads, 2)
               pack2<T>(sc[2 * k2][0], sc[2 * k2][1]), pack2<T>(sc[2 * k2][2], sc[2 * k2][3]),
               pack2<T>(sc[2 * k2 + 1][0], sc[2 * k2 + 1][1]),
               pack2<T>(sc[2 * k2 + 1][2], sc[2 * k2 + 1][3])};
-          // rows past the request's keys hold whatever the page held: as zeros
-          // they add nothing (their weights are 0, but 0 x NaN is not)
-          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-          if (tail)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int key = key0 + k2 * 16 + j * 8 + t2;
-              keep[j] = key + 1 < q.len ? 0xffffffffu : key < q.len ? 0xffffu : 0u;
-            }
 #pragma unroll
           for (int d = 0; d < HD / 16; ++d) {
             uint32_t b[4];
             const int rr = k2 * 16 + vr, ch = (d & 3) * 2 + vc;
             ldsm4t(b, vb + (d >> 2) * kHalfTile + rr * 128 + ((ch ^ (rr & 7)) << 4));
-            if (tail) {
-              b[0] &= keep[0];
-              b[1] &= keep[1];
-              b[2] &= keep[0];
-              b[3] &= keep[1];
-            }
             mma16816<T>(o[2 * d], pf, b[0], b[1]);
             mma16816<T>(o[2 * d + 1], pf, b[2], b[3]);
           }
@@ -425,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
         l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
       }
-      if (NK > 1) {  // join the key groups
+      bool add_back;  // values were taken out
+      {               // join the key groups
         if ((lane & 3) == 0)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -433,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             s_ml[warp][g8 + 8 * j][1] = l[j];
           }
         bar_compute();
+        add_back = s_taken != 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           float M = -INFINITY, L = 0.f;
@@ -487,13 +483,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool whole = w.whole;
       T* outp = static_cast<T*>(a.out);
       if (wk == 0) {
-        unsigned odd[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          bool fin = true;
-#pragma unroll
-          for (int i = 0; i < HD / 8; ++i) fin &= isfinite(o[i][2 * j]) && isfinite(o[i][2 * j + 1]);
-          odd[j] = __ballot_sync(0xffffffffu, !fin && row[j] < R && !isnan(l[j]));
           if (row[j] >= R) continue;
           if (whole) {
             if (mapped) {
@@ -519,32 +510,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         __syncwarp();
-        if ((odd[0] | odd[1]) && mapped) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            // four lanes hold a row: take each row once
-            for (int rr = 0; rr < 8; ++rr) {
-              if (((odd[j] >> (rr * 4)) & 15) == 0) continue;
-              const float mr = __shfl_sync(0xffffffffu, m[j], rr * 4);
-              const float lr = __shfl_sync(0xffffffffu, l[j], rr * 4);
-              const int tk = __shfl_sync(0xffffffffu, tok[j], rr * 4);
-              const int hh = __shfl_sync(0xffffffffu, hg[j], rr * 4);
-              const int pr = __shfl_sync(0xffffffffu, row[j], rr * 4);
-              float acc[HD / 32];
-              if (!masked_key_fallback<T, HD>(a, w.r, w.h, q, kbeg * kKT, kend * kKT, tk, hh,
-                                                   mr == -INFINITY ? 0.f : mr, lane, acc))
-                continue;
-#pragma unroll
-              for (int d = 0; d < HD / 32; ++d) {
-                const int col = lane * (HD / 32) + d;
-                if (whole)
-                  outp[(int64_t)(q.row0 + tk) * a.out_stride +
-                       (int64_t)(w.h * a.G + hh) * HD + col] =
-                      from_f<T>(lr == 0.f ? 0.f : acc[d] / lr);
-                else
-                  a.part_o[((size_t)w.slot * a.tile_rows + pr) * HD + col] = acc[d];
-              }
-            }
+        if (add_back) {
+          // row i from the lanes 4 (i % 8) .. + 3, which hold it, to lane i
+          const float m0 = __shfl_sync(0xffffffffu, m[0], (lane & 7) * 4);
+          const float m1 = __shfl_sync(0xffffffffu, m[1], (lane & 7) * 4);
+          const int ti = a.by_g.div(lane), gi = lane - ti * a.G;
+          void* dst = nullptr;
+          if (lane < R && mapped && whole)
+            dst = outp + (int64_t)(q.row0 + tok0 + ti) * a.out_stride +
+                  (int64_t)(w.h * a.G + gi) * HD;
+          else if (lane < R && mapped)
+            dst = a.part_o + ((size_t)w.slot * a.tile_rows + lane) * HD;
+          add_taken_out<T, HD>(a, w.r, w.h, q, tok0, w.tokens, kbeg * kKT, kend * kKT, lane,
+                               tok0 + ti, gi, lane < 8 ? m0 : m1, dst, !whole, 0, HD);
+          if (lane == 0) s_taken = 0;  // all have read it; set again behind the next meeting
         }
       }
       if (!whole) {

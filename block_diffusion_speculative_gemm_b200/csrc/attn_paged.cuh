@@ -17,6 +17,8 @@
 // planning launch.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -434,64 +436,154 @@ struct AttnWalk {
   __device__ int tokens() const { return min(a.ipt, q.n - t * a.ipt); }
 };
 
-// The accumulators of one row over its visible keys among [from, to0), straight
-// from the pools: out[HD / 32 values a lane, values lane * (HD / 32)..].
-// The tensor-core pass multiplies a masked key's weight, exactly 0, with its
-// value row; where that row holds an infinity or NaN the product poisons rows
-// that do not see the key.  Returns false when no such row exists (then a
-// non-finite result is the row's own).  Called by a warp for a row whose
-// result is not finite, which only such inputs cause.  m: the row's reference
-// maximum in log2 units.  Stops once every column is NaN.
+// Keys that only some rows of an item see.  The tensor-core pass multiplies the
+// weight of a key that a row does not see, exactly 0, with the key's values, and 0
+// times an infinity or NaN would poison the row.  So the values of keys that no row of
+// the item sees are replaced by zeros before the product, and of keys that some rows
+// see the values that are not finite are taken out (as zeros); add_taken_out then adds
+// them to the rows that do see their key.
+struct ItemKeys {
+  int lo, hi;          // some row sees the keys [lo, hi)
+  int all_lo, all_hi;  // all rows see [all_lo, all_hi), which may be empty (all_lo >= all_hi)
+  __device__ ItemKeys(const PagedAttnArgs& a, const AttnReq& q, int tok0, int tokens)
+      : lo(row_lo(a, q.st + tok0)),
+        hi(row_hi(a, q, q.st + tok0 + tokens - 1)),
+        all_lo(row_lo(a, q.st + tok0 + tokens - 1)),
+        all_hi(row_hi(a, q, q.st + tok0)) {}
+};
+
+// The halves of a pair of 16-bit values that are not finite.
+template <typename T> __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
+  constexpr uint32_t E = __is_same(T, __half) ? 0x7c00u : 0x7f80u;
+  return ((v & E) == E ? 0xffffu : 0u) | ((v & (E << 16)) == (E << 16) ? 0xffff0000u : 0u);
+}
+
+// Takes the values that are not finite out of the rows [r0, r1) of a tile of values in
+// shared memory (swizzled 128-byte rows, 64-column halves KT rows apart), and says so in
+// *taken before it does: another warp that finds them gone finds *taken set.  Called by
+// a warp.  0 x v + sum stays 0 as long as every v is finite.
+template <typename T, int HD, int KT>
+__device__ __forceinline__ void take_out(uint8_t* tile, int r0, int r1, int lane, int* taken) {
+  using T2 = std::conditional_t<__is_same(T, __half), __half2, __nv_bfloat162>;
+  const uint32_t zero = 0;
+  const T2 z = *reinterpret_cast<const T2*>(&zero);
+  T2 sum[4] = {z, z, z, z};
+#pragma unroll 1
+  for (int c = r0 * 8 + lane; c < r1 * 8; c += 32)
+#pragma unroll
+    for (int hf = 0; hf < HD / 64; ++hf) {
+      const uint4 w = *reinterpret_cast<const uint4*>(tile + hf * KT * 128 + c * 16);
+      const T2* v = reinterpret_cast<const T2*>(&w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = __hfma2(v[i], z, sum[i]);
+    }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits |= *reinterpret_cast<const uint32_t*>(&sum[i]);
+  __threadfence_block();
+  if (!__any_sync(0xffffffffu, (bits & 0x7fff7fffu) != 0)) return;
+  if (lane == 0) *(volatile int*)taken = 1;
+  __threadfence_block();
+  __syncwarp();
+#pragma unroll 1
+  for (int c = r0 * 8 + lane; c < r1 * 8; c += 32)
+#pragma unroll 1
+    for (int hf = 0; hf < HD / 64; ++hf) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(tile + hf * KT * 128 + c * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] &= ~not_finite<T>(w[i]);
+    }
+}
+
+// Zeros in the rows [r0, r1) of such a tile.
+template <int HD, int KT>
+__device__ __forceinline__ void zero_values(uint8_t* tile, int r0, int r1, int lane) {
+#pragma unroll 1
+  for (int c = r0 * 8 + lane; c < r1 * 8; c += 32)
+#pragma unroll
+    for (int hf = 0; hf < HD / 64; ++hf)
+      *reinterpret_cast<uint4*>(tile + hf * KT * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// The rows [b0, b1) of a tile of values with keys that not every row of the item sees
+// (ItemKeys, relative to the tile's first key).  Called by a warp.
+template <typename T, int HD, int KT>
+__device__ __forceinline__ void edge_values(uint8_t* tile, int b0, int b1, int lo, int hi,
+                                            int all_lo, int all_hi, int lane, int* taken) {
+  lo = max(b0, min(lo, b1));
+  hi = max(lo, min(hi, b1));
+  all_lo = max(lo, min(all_lo, hi));
+  all_hi = max(all_lo, min(all_hi, hi));
+  zero_values<HD, KT>(tile, b0, lo, lane);
+  zero_values<HD, KT>(tile, hi, b1, lane);
+  if (lo < all_lo) take_out<T, HD, KT>(tile, lo, all_lo, lane, taken);
+  if (all_hi < hi) take_out<T, HD, KT>(tile, all_hi, hi, lane, taken);
+}
+
+// Adds what was taken out of the keys [from, to) of an item of `tokens` tokens from
+// tok0 on, to the columns [c0, c1) of its rows: w v for every value v that is not
+// finite of a key that the row sees.  A row a lane: its token, its query head within
+// the group, its reference maximum in log2 units and where its columns are (null: not
+// written), fp32 in a partial and T in the output.  At most 2 (tokens - 1) keys are
+// looked at, however long the context is.  Called by a warp.
 template <typename T, int HD>
-__device__ __noinline__ bool masked_key_fallback(const PagedAttnArgs& a, int r, int h,
-                                                 const AttnReq& q, int from, int to0, int i,
-                                                 int g, float m, int lane, float* out) {
+__device__ __noinline__ void add_taken_out(const PagedAttnArgs& a, int r, int h,
+                                           AttnReq q, int tok0, int tokens, int from, int to,
+                                           int lane, int tok, int g, float ref,
+                                           void* dst, bool partial, int c0, int c1) {
   constexpr int V = HD / 32;
-  const int p = q.st + i;
-  const int to = min(to0, q.len);
-  const int lo = max(from, row_lo(a, p)), hi = min(to, row_hi(a, q, p));
+  const ItemKeys keys(a, q, tok0, tokens);
+  from = max(from, keys.lo);
+  to = min(to, keys.hi);
   const int32_t* tab = a.table + (int64_t)r * a.max_pages;
-  auto row_at = [&](const void* pool, int key) -> const T* {
-    const int e = tab[key / a.page];
-    if (e < 0 || e >= a.n_pages) return nullptr;  // not visible: the tile held zeros there
-    return static_cast<const T*>(pool) +
-           (((int64_t)e * a.nkv + h) * a.page + key % a.page) * HD + lane * V;
-  };
-  bool found = false;
-  for (int key = from; key < to && !found; ++key) {
-    if (key == lo && hi > lo) key = hi;  // the keys it sees are not the question
-    if (key >= to) break;
-    const T* v = row_at(a.v_pool, key);
+  const unsigned on = __ballot_sync(0xffffffffu, dst != nullptr);
+  const int col = lane * V;
+  for (int key = from; key < to; ++key) {
+    if (key >= keys.all_lo && key < keys.all_hi) {
+      key = keys.all_hi - 1;
+      continue;
+    }
+    const int pg = a.by_page.div(key), e = tab[pg];
+    if (e < 0 || e >= a.n_pages) continue;
+    const int64_t at = (((int64_t)e * a.nkv + h) * a.page + key - pg * a.page) * HD + col;
+    const T* vr = static_cast<const T*>(a.v_pool) + at;
+    const T* kr = static_cast<const T*>(a.k_pool) + at;
+    float v[V], k[V];
     bool odd = false;
-    if (v != nullptr)
-#pragma unroll
-      for (int d = 0; d < V; ++d) odd |= !isfinite(to_f(v[d]));
-    found = __any_sync(0xffffffffu, odd);
-  }
-  if (!found) return false;
-  const T* qr = static_cast<const T*>(a.q) + (int64_t)(q.row0 + i) * a.q_stride +
-                (int64_t)(h * a.G + g) * HD + lane * V;
-#pragma unroll
-  for (int d = 0; d < V; ++d) out[d] = 0.f;
-  for (int key = lo; key < hi; ++key) {
-    const T* k = row_at(a.k_pool, key);
-    if (k == nullptr) continue;
-    float s = 0.f;
-#pragma unroll
-    for (int d = 0; d < V; ++d) s += to_f(qr[d]) * to_f(k[d]);
-    s = warp_sum(s);
-    // the weight as the tensor cores would have taken it: rounded to T
-    const float w = to_f(from_f<T>(ex2_ftz(fmaf(s, a.scale_log2, -m))));
-    const T* v = row_at(a.v_pool, key);
-    bool alive = false;
 #pragma unroll
     for (int d = 0; d < V; ++d) {
-      out[d] += w * to_f(v[d]);
-      alive |= !isnan(out[d]);
+      v[d] = to_f(vr[d]);
+      odd |= !isfinite(v[d]);
     }
-    if (!__any_sync(0xffffffffu, alive)) break;
+    if (!__any_sync(0xffffffffu, odd)) continue;
+#pragma unroll
+    for (int d = 0; d < V; ++d) k[d] = to_f(kr[d]);
+    const int p = q.st + tok;
+    unsigned sees = on & __ballot_sync(0xffffffffu, key >= row_lo(a, p) && key < row_hi(a, q, p));
+    for (; sees; sees &= sees - 1) {
+      const int i = __ffs(sees) - 1;
+      const int ti = __shfl_sync(0xffffffffu, tok, i), gi = __shfl_sync(0xffffffffu, g, i);
+      const float ri = __shfl_sync(0xffffffffu, ref, i);
+      void* di = reinterpret_cast<void*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), i));
+      const T* qr = static_cast<const T*>(a.q) + (int64_t)(q.row0 + ti) * a.q_stride +
+                    (int64_t)(h * a.G + gi) * HD + col;
+      float s = 0.f;
+#pragma unroll
+      for (int d = 0; d < V; ++d) s += to_f(qr[d]) * k[d];
+      const float w = ex2_ftz(fmaf(warp_sum(s), a.scale_log2, -ri));
+#pragma unroll
+      for (int d = 0; d < V; ++d) {
+        if (isfinite(v[d]) || col + d < c0 || col + d >= c1) continue;
+        if (partial) {
+          static_cast<float*>(di)[col + d] += w * v[d];
+        } else {
+          T* o = static_cast<T*>(di) + col + d;
+          *o = from_f<T>(to_f(*o) + w * v[d]);
+        }
+      }
+    }
   }
-  return true;
 }
 
 }  // namespace dflash

@@ -269,6 +269,7 @@ struct Seg {
   int run0, runs;
   int slot;        // partial slot
   int mapped;      // the request's pages are (known by seg_info)
+  int taken;       // values were taken out of keys that not every row sees (by o_full)
   __device__ int steps(int x) const { return two ? runs : (runs + 1 - x) >> 1; }
   __device__ int run(int x, int j) const { return run0 + (two ? j : 2 * j + x); }
 };
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full(x), 1);
       mbar_init(p_half(x), 4);  // the tile's warps
       mbar_init(p_full(x), 4);
-      mbar_init(o_full(x), 1);
+      mbar_init(o_full(x), 2);  // the products, and what their warp wrote
       mbar_init(s_read(x), 4);
     }
     for (int k = 0; k < kSegs; ++k) {
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             d.run0 = two ? w.kbeg : max(w.kbeg * 2, w.x.lo >> 7);
             d.runs = (two ? w.kend : min(w.kend * 2, ((w.x.hi - 1) >> 7) + 1)) - d.run0;
             d.slot = w.slot();
+            d.taken = 0;
             mbar_arrive(seg_full(k));
           }
           __syncwarp();
@@ -563,9 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int k = 0; ok; ++k) {
         if (!wait_warp(seg_full(k), phase(k))) { ok = false; break; }
-        const Seg& g = fx.seg[k % kSegs];
+        Seg& g = fx.seg[k % kSegs];
         if (!uniform(g.more)) break;
         const bool two = uniform(g.two);
+        const ItemKeys ik(a, {0, 0, g.st, g.len}, g.tok0, g.tokens);
+        const int lo = uniform(ik.lo), hi = uniform(ik.hi);
+        const int all_lo = uniform(ik.all_lo), all_hi = uniform(ik.all_hi);
         const int n = uniform(g.steps(x)), n0 = uniform(g.steps(0)), n1 = uniform(g.steps(1));
         const int run0 = uniform(g.run0), len = uniform(g.len);
         const uint64_t dq = smem_desc_sw128(s_q + (two ? x : 0) * kTile);
@@ -597,17 +602,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sv = at.slot;
           if (!(ok = wait_warp(full(sv), at.phase))) break;
           at.next(slots);
-          const int live = len - (run0 + (two ? j : 2 * j + x)) * kKT;
-          if (live < kKT) {
-            // Rows past the request's keys hold whatever the page held: as zeros they
-            // add nothing (their weights are 0, but 0 x NaN is not).  With two query
-            // tiles both warps write the zeros.
-            const int rows = kKT - max(live, 0);
-            for (int c = lane; c < rows * 8 * kHalves; c += 32) {
-              const int hf = c / (rows * 8), o = c % (rows * 8);
-              *reinterpret_cast<uint4*>(ring + sv * kTile + hf * kHalfTile + (kKT - rows) * 128 +
-                                        o * 16) = make_uint4(0, 0, 0, 0);
-            }
+          const int key0 = (run0 + (two ? j : 2 * j + x)) * kKT;
+          if (key0 < all_lo || key0 + kKT > all_hi) {
+            // With two query tiles both warps do this, on the same tile.
+            edge_values<T, HD, kKT>(ring + sv * kTile, 0, kKT, lo - key0, hi - key0,
+                                    all_lo - key0, all_hi - key0, lane, &g.taken);
+            // also where the other tile's warp was first to take them out
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
@@ -630,7 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int ks = 4; ks < 8; ++ks)
             umma_ts(on, t_o, t_s + ks * 8, dv + (uint64_t)(ks * 128), id_o, 1u);
           umma_commit_if(on, empty(sv));
-          if (j + 1 == n) umma_commit_if(on, o_full(x));
+          if (j + 1 == n) {
+            mbar_arrive_if(on, o_full(x));
+            umma_commit_if(on, o_full(x));
+          }
         }
         if (!ok) break;
         if (n < n0) {  // a last step without tile 1
@@ -780,7 +783,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t pr = (size_t)g.slot * a.tile_rows + (two ? x * kQT : 0) + lr;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool put = valid && mapped;
-      float odd4[4] = {0.f, 0.f, 0.f, 0.f};  // not 0 once a value is not finite
       if (live) {
 #pragma unroll 1
         for (int cc = c0; cc < c0 + nc; cc += 32) {
@@ -796,8 +798,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], f1, o[i]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) odd4[i & 3] = fmaf(o[i], 0.f, odd4[i & 3]);
           if (!put) continue;
           if (whole) {
             uint32_t u[16];
@@ -821,31 +821,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (a.lse)
           a.lse[orow * a.nq + hd] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       }
-      const bool fin = odd4[0] + odd4[1] + (odd4[2] + odd4[3]) == 0.f;
-      unsigned odd = __ballot_sync(0xffffffffu, !fin && put && !isnan(l));
-      for (; odd; odd &= odd - 1) {
-        const int src = __ffs(odd) - 1;
-        const float mr = __shfl_sync(0xffffffffu, m, src), lr2 = __shfl_sync(0xffffffffu, l, src);
-        const int tk2 = __shfl_sync(0xffffffffu, tk, src), hd2 = __shfl_sync(0xffffffffu, hd, src);
-        float acc[HD / 32];
-        AttnReq rq;
-        attn_req(a, g.r, rq);
-        if (!masked_key_fallback<T, HD>(a, g.r, g.h, rq, g.run0 * kKT, (g.run0 + g.runs) * kKT,
-                                        tk2, hd2 - g.h * a.G, mr == -INFINITY ? 0.f : mr, lane,
-                                        acc))
-          continue;
-        T* o2 = static_cast<T*>(a.out) + (int64_t)(g.row0 + tk2) * a.out_stride +
-                (int64_t)hd2 * HD;
-        const size_t pr2 = pr - lane + src;
-#pragma unroll
-        for (int d = 0; d < HD / 32; ++d) {
-          const int col = lane * (HD / 32) + d;
-          if (col < c0 || col >= c0 + nc) continue;  // the row's other thread does those
-          if (whole)
-            o2[col] = from_f<T>(lr2 == 0.f ? 0.f : acc[d] / lr2);
-          else
-            a.part_o[pr2 * HD + col] = acc[d];
-        }
+      if (g.taken && mapped && live) {
+        __syncwarp();
+        void* dst = nullptr;
+        if (put) dst = whole ? static_cast<void*>(outp) : a.part_o + pr * HD;
+        add_taken_out<T, HD>(a, g.r, g.h, {g.row0, 0, g.st, g.len}, g.tok0, g.tokens,
+                             g.run0 * kKT, (g.run0 + g.runs) * kKT, lane, tk, hd - g.h * a.G, m,
+                             dst, !whole, c0, c0 + nc);
       }
       // both threads of a row have read maximum, sum and accumulators
       if (!two && !meet_rows()) { ok = false; break; }
