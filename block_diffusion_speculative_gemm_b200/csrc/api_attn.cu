@@ -173,7 +173,10 @@ extern "C" size_t dflash_attention_paged_workspace_size(int batch, int n_rows, i
       (head_dim != 64 && head_dim != 128))
     return 0;
   if (batch == 0 || n_rows == 0) return kHeader;
-  return attn_layout(batch, n_rows, n_q / n_kv, head_dim).end;
+  // The kernel goes by the average request, and the one for longer requests needs more:
+  // as for one request that has all rows, so that the workspace of the largest batch and
+  // row count serves every call with fewer of either.
+  return attn_layout(1, n_rows, n_q / n_kv, head_dim).end;
 }
 
 extern "C" int dflash_attention_paged(const void* q, int64_t q_stride, int dtype,

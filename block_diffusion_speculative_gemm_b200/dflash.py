@@ -644,7 +644,8 @@ def attention_paged_workspace_size(batch: int, n_rows: int, n_q: int, n_kv: int,
 
 def attention_paged_workspace(batch: int, n_rows: int, n_q: int, n_kv: int, head_dim: int,
                               device=None, stream=None) -> torch.Tensor:
-    """A workspace for ``attention_paged`` calls of this shape, and for the two row operators."""
+    """A workspace for ``attention_paged`` calls of at most ``batch`` requests and ``n_rows``
+    rows, and for the two row operators."""
     n = attention_paged_workspace_size(batch, n_rows, n_q, n_kv, head_dim)
     if n == 0:
         raise DFlashError("dflash_attention_paged_workspace_size", EUNSUPPORTED)

@@ -512,8 +512,9 @@ int dflash_kv_append_paged(const void* k, int64_t k_stride, const void* v, int64
                            int n_pages, int page_size, const int32_t* page_table, int max_pages,
                            void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace of one dflash_attention_paged call (0 for shapes that the
- * call does not support). */
+/* Bytes of workspace of a dflash_attention_paged call of at most `batch` requests and
+ * n_rows rows, also with fewer of either (0 for shapes that the call does not
+ * support). */
 size_t dflash_attention_paged_workspace_size(int batch, int n_rows, int n_q, int n_kv,
                                              int head_dim);
 
