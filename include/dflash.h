@@ -514,7 +514,7 @@ int dflash_kv_append_paged(const void* k, int64_t k_stride, const void* v, int64
 
 /* Bytes of workspace of a dflash_attention_paged call of at most `batch` requests and
  * n_rows rows, also with fewer of either (0 for shapes that the call does not
- * support). */
+ * support; the header's size for n_rows 0, whatever the batch). */
 size_t dflash_attention_paged_workspace_size(int batch, int n_rows, int n_q, int n_kv,
                                              int head_dim);
 
