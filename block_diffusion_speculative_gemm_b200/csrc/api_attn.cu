@@ -173,7 +173,7 @@ extern "C" size_t dflash_attention_paged_workspace_size(int batch, int n_rows, i
       (head_dim != 64 && head_dim != 128))
     return 0;
   if (batch == 0 || n_rows == 0) return kHeader;
-  if (batch > kAttnMaxBatch || n_rows > kAttnMaxRows) return 0;
+  if (batch > kPagedMaxBatch || n_rows > kPagedMaxRows) return 0;
   // The kernel goes by the average request, and the one for longer requests needs more:
   // as for one request that has all rows, so that the workspace of the largest batch and
   // row count serves every call with fewer of either.
@@ -193,7 +193,7 @@ extern "C" int dflash_attention_paged(const void* q, int64_t q_stride, int dtype
   if (!(scale > 0.f) || !isfinite(scale) || window < 0) return DFLASH_EINVAL;
   if (!elem_size(dtype)) return DFLASH_EINVAL;
   if (dtype == DFLASH_F32 || (head_dim != 64 && head_dim != 128) || n_q / n_kv > 64 ||
-      batch > kAttnMaxBatch || n_rows > kAttnMaxRows)
+      batch > kPagedMaxBatch || n_rows > kPagedMaxRows)
     return DFLASH_EUNSUPPORTED;
   if (n_rows == 0) return DFLASH_OK;
   if (!cu_rows || !start_pos || !rows_ok(q, q_stride, n_q, head_dim, 2) ||

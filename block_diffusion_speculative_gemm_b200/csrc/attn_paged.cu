@@ -612,7 +612,7 @@ int launch_one(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap&
   constexpr int kFixed = 1024 + kSlots * slot_bytes<HD>() + kScratch;
   static SmemLimit limit;
   if (!limit.raise(reinterpret_cast<const void*>(attn_paged_kernel<T, HD>),
-                   kFixed + kAttnMaxBatch * 8))
+                   kFixed + kPagedMaxBatch * 8))
     return DFLASH_ECUDA;
   const cudaError_t e =
       launch_pdl(attn_paged_kernel<T, HD>, dim3(attn_paged_ctas()), dim3(kThreads),

@@ -192,9 +192,9 @@ __device__ long long attn_units(const PagedAttnArgs& a, int r, const AttnReq& q,
 }
 
 // Largest batch of a call: the prefix sums of every request sit in shared memory.
-constexpr int kAttnMaxBatch = 4096;
+constexpr int kPagedMaxBatch = 4096;
 // Largest row count: row and item arithmetic stays inside 31 bits.
-constexpr int kAttnMaxRows = 1 << 30;
+constexpr int kPagedMaxRows = 1 << 30;
 
 // Fills pre[r] with the units of requests 0..r (every thread of the CTA; ends
 // with a barrier).  Requests with bad lengths or rows out of order have none and set
