@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
               for (int i = 0; i < HD / 8; ++i)
                 *reinterpret_cast<uint32_t*>(dst + i * 8) =
-                    pack2<T>(o[i][2 * j] * inv, o[i][2 * j + 1] * inv);
+                    pack_result<T>(o[i][2 * j] * inv, o[i][2 * j + 1] * inv);
               if (a.lse && (lane & 3) == 0)
                 a.lse[(int64_t)(q.row0 + tok[j]) * a.nq + w.h * a.G + hg[j]] =
                     l[j] == 0.f ? -INFINITY : (m[j] + log2f(l[j])) * 0.6931471805599453f;
@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             T* dst = outp + (int64_t)(q.row0 + tk) * a.out_stride + (int64_t)hh * HD + lane * V;
 #pragma unroll
             for (int i = 0; i < V; i += 2)
-              *reinterpret_cast<uint32_t*>(dst + i) = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+              *reinterpret_cast<uint32_t*>(dst + i) =
+                  pack_result<T>(acc[i] * inv, acc[i + 1] * inv);
             if (a.lse && lane == 0)
               a.lse[(int64_t)(q.row0 + tk) * a.nq + hh] =
                   L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;

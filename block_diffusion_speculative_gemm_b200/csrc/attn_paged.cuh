@@ -34,6 +34,17 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A pair of results.  An average of fp16 values never leaves their range, but its weights
+// are rounded and the sum they are divided by is not, which could take it past the
+// largest value by 2^-11 of it: finite results are held inside the range.
+template <typename T> __device__ __forceinline__ uint32_t pack_result(float lo, float hi) {
+  if constexpr (__is_same(T, __half)) {
+    if (fabsf(lo) < INFINITY) lo = fminf(fmaxf(lo, -65504.f), 65504.f);
+    if (fabsf(hi) < INFINITY) hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+  }
+  return pack2<T>(lo, hi);
+}
+
 // Quotients by a number that is known at launch, for dividends below 2^31
 // (Granlund and Montgomery: with 2^s >= d and m = ceil(2^(31+s) / d), n / d is
 // floor(n m / 2^(31+s))).

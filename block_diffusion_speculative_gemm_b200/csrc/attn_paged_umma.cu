@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (whole) {
             uint32_t u[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
+            for (int i = 0; i < 16; ++i) u[i] = pack_result<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
             store32(outp + cc, u, a.wide_out);
             store32(outp + cc + 16, u + 8, a.wide_out);
           } else {
@@ -913,8 +913,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < V; ++i)
     *reinterpret_cast<uint2*>(dst + 4 * (sub + 8 * i)) =
-        make_uint2(pack2<T>(acc[i].x * inv, acc[i].y * inv),
-                   pack2<T>(acc[i].z * inv, acc[i].w * inv));
+        make_uint2(pack_result<T>(acc[i].x * inv, acc[i].y * inv),
+                   pack_result<T>(acc[i].z * inv, acc[i].w * inv));
   if (a.lse && sub == 0)
     a.lse[tok * a.nq + head] =
         L == 0.f ? -INFINITY : (ref + log2f(L)) * 0.6931471805599453f;

@@ -477,8 +477,9 @@ int dflash_verify_noalloc(const void* target_logits, int logits_dtype,
  *                (the first two calls need the header alone: that size for n_rows 0),
  *                zero-filled once as every workspace.
  * Arithmetic is fp32, rounded once on the way out (attention's softmax weights also
- * once, to the operands' type, in front of the second product).  An fp16 result
- * that overflows sets DFLASH_DEV_RANGE.  A request with a page in use unmapped
+ * once, to the operands' type, in front of the second product).  An fp16 result of
+ * the first two calls that overflows sets DFLASH_DEV_RANGE; attention averages values
+ * and keeps finite results inside their range.  A request with a page in use unmapped
  * writes nothing and sets DFLASH_DEV_PAGE; one whose rows leave the rotation
  * table or the cache writes nothing and sets DFLASH_DEV_CTX_CAP; the others are
  * not affected.  After DFLASH_DEV_TIMEOUT zero-fill the workspace again.
