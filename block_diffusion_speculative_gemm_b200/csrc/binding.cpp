@@ -126,6 +126,8 @@ struct Call {
     const at::Tensor& t = whole(o, "rope", at::kFloat);
     if (t.dim() != 3 || t.size(0) != 2 || t.size(2) * 2 != hd)
       bad_value("rope must be [2, max_pos, head_dim / 2]");
+    // without positions it has no address, which would stand for no rotation
+    if (t.size(1) < 1) bad_value("rope has no positions");
     max_pos = count(t.size(1), "rope");
     return static_cast<const float*>(t.const_data_ptr());
   }
