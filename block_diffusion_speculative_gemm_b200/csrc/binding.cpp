@@ -189,6 +189,13 @@ int integer(PyObject* o, const char* name) {
   return (int)v;
 }
 
+// Gives up the interpreter lock while it lives: a launch can wait for room in its
+// stream's queue, and the work in front of it for a host function in Python.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs f, turning what it throws into a Python exception.
 template <typename F>
 PyObject* guarded(const char* name, Py_ssize_t have, Py_ssize_t want, F f) {
@@ -239,12 +246,14 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& ws = c.whole(a[9], "ws", at::kByte);
     const float eps = (float)number(a[10]);
     const int nq = has_q ? c.count(q->size(1), "q") : 0, nkv = has_k ? c.count(k->size(1), "k") : 0;
+    const int hd = c.count(t.size(2), "q"), n_rows = c.count(t.size(0), "q");
+    void* const stream = c.stream(a[11]);
     need_bound((const void*)g_qk);
+    const Unlocked unlocked;
     return g_qk(nq ? q->const_data_ptr() : nullptr, qs, nkv ? k->const_data_ptr() : nullptr, ks,
-                dt, gq, gk, eps, rope, max_pos, cu, st, batch, c.count(t.size(0), "q"), nq, nkv,
-                c.count(t.size(2), "q"), nq ? qo->data_ptr() : nullptr, qos,
-                nkv ? ko->data_ptr() : nullptr, kos, ws.data_ptr(), (size_t)ws.numel(),
-                c.stream(a[11]));
+                dt, gq, gk, eps, rope, max_pos, cu, st, batch, n_rows, nq, nkv, hd,
+                nq ? qo->data_ptr() : nullptr, qos, nkv ? ko->data_ptr() : nullptr, kos,
+                ws.data_ptr(), (size_t)ws.numel(), stream);
   });
 }
 
@@ -264,11 +273,13 @@ PyObject* kv_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Call::Pool p = c.pool(a[6], a[7], a[8], k.size(2), k.size(1), batch);
     const at::Tensor& ws = c.whole(a[9], "ws", at::kByte);
     const float eps = (float)number(a[10]);
+    const int hd = c.count(k.size(2), "k"), n_rows = c.count(k.size(0), "k");
+    void* const stream = c.stream(a[11]);
     need_bound((const void*)g_append);
+    const Unlocked unlocked;
     return g_append(k.const_data_ptr(), ks, v.const_data_ptr(), vs, dt, gk, eps, rope, max_pos, cu,
-                    st, batch, c.count(k.size(0), "k"), p.n_kv, c.count(k.size(2), "k"), p.k, p.v,
-                    p.dtype, p.n_pages, p.page, p.table, p.max_pages, ws.data_ptr(),
-                    (size_t)ws.numel(), c.stream(a[11]));
+                    st, batch, n_rows, p.n_kv, hd, p.k, p.v, p.dtype, p.n_pages, p.page, p.table,
+                    p.max_pages, ws.data_ptr(), (size_t)ws.numel(), stream);
   });
 }
 
@@ -297,11 +308,14 @@ PyObject* attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float scale = (float)(a[9] == Py_None ? 1.0 / std::sqrt((double)hd) : number(a[9]));
     const int causal = PyObject_IsTrue(a[10]);
     if (causal < 0) throw Raised{};
+    const int window = integer(a[11], "window");
+    const int n_rows = c.count(q.size(0), "q"), nq = c.count(q.size(1), "q");
+    void* const stream = c.stream(a[13]);
     need_bound((const void*)g_attn);
-    return g_attn(q.const_data_ptr(), qs, dt, cu, st, len, batch, c.count(q.size(0), "q"),
-                  c.count(q.size(1), "q"), p.n_kv, hd, p.k, p.v, p.n_pages, p.page, p.table,
-                  p.max_pages, scale, causal, integer(a[11], "window"), out.data_ptr(), os, lse,
-                  ws.data_ptr(), (size_t)ws.numel(), c.stream(a[13]));
+    const Unlocked unlocked;
+    return g_attn(q.const_data_ptr(), qs, dt, cu, st, len, batch, n_rows, nq, p.n_kv, hd, p.k, p.v,
+                  p.n_pages, p.page, p.table, p.max_pages, scale, causal, window, out.data_ptr(),
+                  os, lse, ws.data_ptr(), (size_t)ws.numel(), stream);
   });
 }
 
