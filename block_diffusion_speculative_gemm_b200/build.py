@@ -85,6 +85,20 @@ def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = 
     return lib
 
 
+def binding_key() -> str:
+    """What a build of csrc/binding.cpp belongs to; it holds this text (kBuiltFor)."""
+    import torch
+
+    return (f"built for {sys.implementation.cache_tag}, torch {torch.__version__}, "
+            f"C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}.")
+
+
+def binding_current() -> bool:
+    """True when _calls.so was built for this Python and torch."""
+    with open(BINDING, "rb") as f:
+        return binding_key().encode() in f.read()
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Compiles csrc/binding.cpp against this Python's and torch's headers."""
     import sysconfig
@@ -94,14 +108,15 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
     deps = [BINDING_SRC, os.path.join(INCLUDE, "dflash.h"), __file__]
     if not force and os.path.exists(BINDING) and all(
-            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+            os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps) and binding_current():
         return BINDING
     nvcc_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))),
                                 "include")
     inc = [INCLUDE, sysconfig.get_paths()["include"], nvcc_include, *include_paths()]
     tmp = BINDING + ".tmp"
     _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-          "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-fvisibility=hidden", f'-DDFLASH_BUILT_FOR="{binding_key()}"',
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *[f"-isystem{p}" for p in inc], "-o", tmp, BINDING_SRC,
           *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
           "-lc10"], verbose)

@@ -345,4 +345,8 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, kMethods,
 
 }  // namespace
 
+// The Python and torch that this module's types are of: looked for in the file before it
+// is loaded.
+extern "C" __attribute__((visibility("default"), used)) const char kBuiltFor[] = DFLASH_BUILT_FOR;
+
 PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&kModule); }

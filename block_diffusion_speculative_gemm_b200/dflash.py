@@ -615,6 +615,11 @@ def calls():
     """The module of these operators' calls (csrc/binding.cpp), bound to the loaded library."""
     global _calls
     if _calls is None:
+        from . import build as _build
+
+        if os.path.exists(_build.BINDING) and not _build.binding_current():
+            raise RuntimeError("_calls.so was built for another Python or torch: build it again "
+                               "with `python -m block_diffusion_speculative_gemm_b200.build`")
         try:
             from . import _calls as m
         except ImportError as e:
