@@ -257,9 +257,18 @@ class Model:
         return new_workspace(self.workspace_size(max_batch, B, max_inject_rows), device)
 
 
+def _empty_on(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor for work on ``stream`` (None: the current one).  Its memory is
+    of that stream: the current one's may still be in use by work queued there."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device or "cuda")
+
+
 def new_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     """A zero-filled, 256-byte aligned device workspace of ``nbytes`` bytes."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
+    ws = _empty_on(max(int(nbytes), 256), torch.uint8, device, stream)
     assert ws.data_ptr() % 256 == 0
     _check("dflash_workspace_init", lib().dflash_workspace_init(_ptr(ws), ws.numel(),
                                                                 _stream(stream)))
@@ -634,7 +643,7 @@ def calls():
 
 def rope_table(max_pos: int, head_dim: int, base: float, device=None, stream=None) -> torch.Tensor:
     """Rotation table [2, max_pos, head_dim / 2] (cosines, sines) of angle p * base^(-2i/head_dim)."""
-    t = torch.empty((2, max_pos, head_dim // 2), dtype=torch.float32, device=device or "cuda")
+    t = _empty_on((2, max_pos, head_dim // 2), torch.float32, device, stream)
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"the table must be on the current CUDA device, is on {t.device}")
     _check("dflash_rope_table", lib().dflash_rope_table(t.data_ptr(), max_pos, head_dim,
