@@ -97,6 +97,8 @@ __device__ __forceinline__ int attn_req(const PagedAttnArgs& a, int r, AttnReq& 
   q.st = a.start[r];
   if (out_of_order(q.row0, end, a.n_rows)) return DFLASH_DEV_ROWS;
   q.n = end - q.row0;
+  q.len = 0;
+  if (q.n == 0) return 0;  // a free place of a padded batch: its lengths are not looked at
   const int64_t last = (int64_t)q.st + q.n;
   const int64_t len = a.kv_len ? (int64_t)a.kv_len[r] : last;
   if (q.st < 0 || last > 0x7fffffff || len < 0 || len > (int64_t)a.max_pages * a.page)

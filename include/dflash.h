@@ -460,7 +460,8 @@ int dflash_verify_noalloc(const void* target_logits, int logits_dtype,
  *                cu_rows[batch] up to n_rows are padding: nothing of theirs is
  *                written.  A request whose rows are not an ascending range inside
  *                [0, n_rows], or which starts below an earlier entry, writes nothing
- *                and sets DFLASH_DEV_ROWS.
+ *                and sets DFLASH_DEV_ROWS.  Nothing else of a request without rows is
+ *                looked at.
  *   start_pos    device int32 [batch]: position of request r's first row.
  *   rope         device fp32 [2][max_pos][head_dim/2], the cosines then the sines of
  *                every position's angles (dflash_rope_table, or a caller's own, for
