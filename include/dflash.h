@@ -76,10 +76,11 @@ extern "C" {
 #define DFLASH_DEV_OUT_CAP     2  /* verify output would pass out_cap */
 #define DFLASH_DEV_TOKEN_RANGE 4  /* token id outside [0, V) */
 #define DFLASH_DEV_TIMEOUT     8  /* a bounded device wait expired */
-#define DFLASH_DEV_ROWS        16 /* cu_rows not monotone or not ending at n_rows */
+#define DFLASH_DEV_ROWS        16 /* cu_rows not monotone, or (injection) not ending at n_rows */
 #define DFLASH_DEV_PAGE        32 /* a position's page-table entry is unmapped (paged K/V) */
-#define DFLASH_DEV_RANGE       64 /* an fp16 activation or cache entry overflowed (bf16 models) */
-#define DFLASH_DEV_CHECK      128 /* bounds-checked build only: an index failed its check */
+#define DFLASH_DEV_RANGE       64 /* an fp16 activation, result or cache entry overflowed */
+#define DFLASH_DEV_CHECK      128 /* an index failed its check (bounds-checked build), or a
+                                    kernel's on-chip memory was not where it has to be */
 
 /* ---- element types ---------------------------------------------------- */
 #define DFLASH_F32  0
