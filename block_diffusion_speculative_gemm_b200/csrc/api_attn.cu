@@ -52,12 +52,14 @@ int check_pool(const void* k_pool, const void* v_pool, int cache_dtype, int n_kv
   return DFLASH_OK;
 }
 
-// Rows of an item tile: the average request's rows decide.  Any tile is right
-// for any mix of lengths; 256 is the tcgen05 kernel's pair of query tiles.  With
-// 4 rows (32 requests of one token, 4 query heads a key head) the mma.sync kernel
-// takes 49 us and the tcgen05 kernel 53, one request of one token 12 and 17; with
-// 32 rows (blocks of 8) the former took 67 and the latter takes 53, with 64 rows
-// 172 and 93.
+// Rows of an item tile: the average request's rows decide.  Either kernel is correct for
+// any mix of lengths; 256 is the tcgen05 kernel's pair of query tiles.  With 4 rows
+// (32 requests of one token, 4 query heads a key head) the mma.sync kernel takes 50 us
+// and the tcgen05 kernel 53, 256 of them 380 and 400, one request of one token 13 and
+// 18; with 32 rows (32 blocks of 8) the former 86 and the latter 55, with 64 rows (4
+// blocks of 16 behind 32768 keys) 314 and 94.  The average is not the best choice where
+// one chunk stands among many single tokens: 63 and a chunk of 128 behind 4096 keys take
+// 203 us in the kernel chosen and 182 in the other, 255 and a chunk of 512 978 and 812.
 int pick_tile_rows(int batch, int n_rows, int G) {
   const int64_t rows = std::max<int64_t>(((int64_t)n_rows + batch - 1) / batch * G, G);
   return rows <= 16 ? 16 : 256;

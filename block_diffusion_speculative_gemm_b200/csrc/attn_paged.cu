@@ -13,9 +13,11 @@
 // operand without leaving the thread.  Bound by memory: the keys and values of an
 // item are read once for all its rows, 4 rows flop per byte.  The producer runs on
 // over segment boundaries, so the ring stays full while a segment is finished, and
-// two CTAs share an SM.  32 single tokens behind 512 to 4096 keys (32 query, 8 key
-// heads of 128): 49 us, 5.4 TB/s with start and end; one token behind 2048 keys: 12 us,
-// a chain of loads (lengths, page table, keys, partials).
+// two CTAs share an SM; at head_dim 128 the requests' sums of units leave room for one
+// from 198 requests on, which streams as fast (198 single tokens 297 us, 197 294).
+// 32 single tokens behind 512 to 4096 keys (32 query, 8 key heads of 128): 50 us, 5.3
+// TB/s with start and end, 256 of them 6.3 TB/s; one token behind 2048 keys: 12.5 us, a
+// chain of loads (lengths, page table, keys, partials).
 //
 // Every CTA has the same number of key tiles (attn_paged.cuh); an item shared
 // by several CTAs is left as partials (O, max, sum), and the CTA that counts

@@ -26,9 +26,10 @@
 // Bound by the tensor cores and, equally, by the exponentials: 4 x 128 x 128 x
 // HD flop and 128 x 128 exponentials a tile, 1024 cycles each at head_dim 128; a step
 // of both tiles takes about 3000 cycles, since a tile's S, softmax and P V follow one
-// another.  A prompt of 8192 tokens (32 query, 8 key heads of 128): 455 us, 1.2
-// PFLOP/s, 515 us once the clocks drop; 4 blocks of 16 behind 32768 keys: 93 us, 5.8
-// TB/s.  (Evaluating a quarter of the exponentials by a polynomial on the FMA pipe was
+// another.  On new inputs each time, a prompt of 8192 tokens (32 query, 8 key heads of
+// 128) takes 528 us, 1.04 PFLOP/s at the clocks that the power limit leaves; 4 blocks of
+// 16 behind 32768 keys 106 us, 5.1 TB/s; 32 blocks of 8 behind 512 to 4096 keys 58 us.
+// (Evaluating a quarter of the exponentials by a polynomial on the FMA pipe was
 // slower: 512 us against 497 for a prompt of 8192 tokens; its instructions cost
 // more issue slots than the special-function unit's time is worth.)
 #include <algorithm>

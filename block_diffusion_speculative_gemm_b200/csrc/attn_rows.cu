@@ -365,8 +365,11 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const RowArgs p) {
 // flight per SM without a register.  Compute warp w of W takes the rows w, w + W, ...
 // in two stages of its own (a stage that changed hands could be waited for a whole
 // round early) and writes its results straight from registers.  16384 rows of 32
-// query and 8 key heads of 128 bf16: 64 us (5.4 TB/s), against 91 with a thread's
-// loads behind its lookups; their append to a bf16 cache 27 us against 50.
+// query and 8 key heads of 128 bf16: 65 us (5.3 TB/s), against 91 with a thread's
+// loads behind its lookups; their append to a bf16 cache 28 us against 50.  The ring
+// holds whole rows, at least 16: rows of more than 53 heads of 128 in 16 bits or 26 in
+// fp32 (about twice as many of 64) take the other kernel (64 / 8 bf16 132 us, 32 / 8 fp32 133 us,
+// 4.6 and 5.1 TB/s).
 constexpr int kStreamMax = 32;  // stages, two a warp
 constexpr int kStreamSmem = 220 * 1024;
 
