@@ -8,7 +8,7 @@ import torch
 
 from block_diffusion_speculative_gemm_b200 import dflash as D
 
-from .test_attention_paged_gpu import F, T, cu_of, gen, i32, randn
+from .test_attention_paged_gpu import F, Case, T, cu_of, gen, i32, randn
 
 pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
@@ -111,3 +111,28 @@ def test_keys_and_values_full_of_nan_that_later_rows_see(rows):
     half = rows - rows // 2
     assert torch.equal(out[1, :half], out[0, :half])
     assert torch.isnan(out[1, half:]).all() and torch.isfinite(out[0]).all()
+
+
+@pytest.mark.parametrize("dtype,hd,page", [("bf16", 128, 64), ("f16", 64, 16)])
+@pytest.mark.parametrize("rows", [[1, 3], [1] * 40, [33, 9], [300, 70, 1]])
+def test_stored_keys_that_no_row_sees(dtype, hd, page, rows):
+    # more keys stored than the causal rows see, and keys behind a window: NaN in all of them, and
+    # pages that hold nothing else not mapped
+    ctx = [50 + 23 * r for r in range(len(rows))]
+    end = [a + b for a, b in zip(rows, ctx)]
+    c = Case(hd + len(rows), rows, ctx, 8, 2, hd, dtype, page, kv_len=[t + 137 for t in end])
+    c.check(*c.run(False), False)
+    for window in (0, 45):
+        want = c.run(True, window)
+        c.check(*want, True, window)
+        d = Case(hd + len(rows), rows, ctx, 8, 2, hd, dtype, page, kv_len=[t + 137 for t in end])
+        for r, t in enumerate(end):
+            first = max(0, ctx[r] - window + 1) if window else 0
+            for key in [*range(first), *range(t, t + 137)]:
+                at = int(d.tab[r, key // page])
+                d.kp[at, :, key % page] = NAN
+                d.vp[at, :, key % page] = NAN
+            d.tab[r, : first // page] = -1
+            d.tab[r, -(-t // page):] = d.n_pages
+        got = d.run(True, window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
